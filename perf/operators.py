@@ -206,8 +206,8 @@ def prepare(case, seed):
             rest = torch.randperm(nodes - n, generator=cpu)[:n - first].sort().values + n
             first = n - len(rest)
             acc[s, :n] = torch.cat([torch.arange(first), rest]).to(torch.int32)
-        st.update(pools=pools, k_pools=[p[0] for p in pools], v_pools=[p[1] for p in pools],
-                  tables=bt.to(dev), ctx=torch.tensor(ctx, dtype=torch.int32, device=dev),
+        st.update(pools=pools, k_pools=pools[:, 0], v_pools=pools[:, 1], tables=bt.to(dev),
+                  ctx=torch.tensor(ctx, dtype=torch.int32, device=dev),
                   lens=torch.full((S,), nodes, dtype=torch.int32, device=dev),
                   accepted=acc.to(dev), n_accepted=n_acc.to(dev))
     return st
