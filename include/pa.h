@@ -195,6 +195,62 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
                           void* stream);
 
 /*
+ * pa_decode_tree -- decode with a tree of drafted tokens per sequence, as when
+ * the draft offers several continuations and the target model checks all of
+ * them in one pass ([P1] §五 "Speculative Decoding"; [P3] "推測解碼": the
+ * guesses are checked in parallel; a chain of guesses is pa_decode_multi).
+ * The K/V of the tree's n_s = tree_lens[s] nodes must already be in the cache,
+ * node j at position P_s + j, where P_s = context_lens[s] - n_s is the prefix
+ * (context_lens counts the nodes).  Node i attends to the whole prefix and to
+ * the nodes its mask names, itself only if bit i is set:
+ *     out[s][i][h] = softmax over {keys < P_s} and {P_s + j : bit j of
+ *                    masks[s][i]} of (scale * q[s][i][h] . K_s), times V_s
+ * Any mask is taken (pa_tree_masks makes those of a tree from its parents);
+ * bits n_s .. 63 are ignored.  A row that attends to nothing is all zeros,
+ * and so are the rows n_s .. q_len - 1 of a sequence with fewer nodes.  With
+ * context_lens[s] < n_s the first nodes have no position and are seen by
+ * nobody.  What lies in the cache past the context is never used.
+ *
+ *   out, q       device [num_seqs][q_len][n_q_heads][head_dim], dtype q_dtype
+ *   q_len        1 .. 64, the most nodes of a sequence
+ *   masks        device uint64 [num_seqs][q_len], 8-byte aligned
+ *   tree_lens    device int32 [num_seqs], each in [0, q_len]; NULL: all q_len.
+ *                A value outside is clamped and flagged (PA_DEVERR_QUERY_LOC)
+ *   workspace    >= pa_decode_tree_workspace_size(num_seqs, q_len, n_q_heads,
+ *                n_kv_heads, head_dim) bytes, 16-byte aligned (may be NULL
+ *                when that size is 0); scratch, contents on entry ignored;
+ *                calls that may overlap need one each
+ *   other arguments as pa_decode.
+ *
+ * Supported as pa_decode (head_dim 64 or 128, group size <= 8, 16-bit caches
+ * of the query's type and fp8 caches) except q_dtype PA_F32
+ * (PA_ERR_UNSUPPORTED).  A block id outside [0, num_blocks) is flagged with
+ * PA_DEVERR_BLOCK_ID and its keys read as zeros.
+ */
+size_t pa_decode_tree_workspace_size(int num_seqs, int q_len, int n_q_heads, int n_kv_heads,
+                                     int head_dim);
+pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* context_lens,
+                         const uint64_t* masks, const int32_t* tree_lens, float scale,
+                         int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                         int num_seqs, int q_len, int max_blocks_per_seq, int num_blocks,
+                         pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale, float v_scale,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                         void* stream);
+
+/*
+ * pa_tree_masks -- host helper for pa_decode_tree: the masks of trees given by
+ * their parents.  parents[s][i] is the parent of node i, a lower index, or -1
+ * for a node that continues the prefix; masks_out[s][i] gets the bits of node
+ * i and all its ancestors, and 0 for i >= tree_lens[s] (tree_lens NULL: none).
+ * PA_ERR_INVALID_ARG for a parent outside [-1, i - 1], q_len outside 1 .. 64 or
+ * a tree_lens entry outside [0, q_len]; masks_out is then left as it was.
+ *   parents, tree_lens, masks_out  host memory
+ */
+pa_status pa_tree_masks(const int32_t* parents, const int32_t* tree_lens, int num_seqs,
+                        int q_len, uint64_t* masks_out);
+
+/*
  * pa_decode_shared_prefix -- pa_decode's result, reading each block that a
  * group of sequences shares at the start of their tables once for the whole
  * group: the samples of one prompt share its blocks ([P1] §三.2: parallel
@@ -375,6 +431,42 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
                            float v_scale, void* workspace, size_t workspace_bytes,
                            int32_t* dev_err, void* stream);
 
+/*
+ * pa_prefill_packed -- attention over whole prompts that lie one behind
+ * another in q, k and v, as the projections of a step that admits several
+ * requests leave them ([P1] §一.1: the prompt's tokens are processed in one
+ * pass; [P1] §二 Attention formula).  It reads no cache: pa_reshape_and_cache
+ * stores the same K/V for the decode steps, before or after this call.
+ * Sequence s owns rows query_start_loc[s] .. query_start_loc[s + 1] - 1; row r
+ * attends to the rows of its own sequence up to and including itself:
+ *     out[r][h] = softmax(scale * q[r][h] . K^T, causal) . V
+ * with K, V of kv head h / (n_q_heads / n_kv_heads).  Rows of out outside every
+ * sequence (a padded batch) are left as they are, and what q, k and v hold
+ * there is not used; sequences may be empty.
+ *
+ *   out            device [total_tokens][n_q_heads][head_dim], packed
+ *   q, k, v        device, token t at element t * stride: [n_q_heads] resp.
+ *                  [n_kv_heads][head_dim] elements, so the parts of one fused
+ *                  projection need no copy; strides in elements, multiples of
+ *                  8, not below the token's own size
+ *   query_start_loc device int32 [num_seqs + 1], non-decreasing, within
+ *                  [0, total_tokens].  An entry that is not is flagged with
+ *                  PA_DEVERR_QUERY_LOC, its sequence clamped to the tensors
+ *   total_tokens   rows of out, q, k and v
+ *
+ * Supported: dtype F16 or BF16 (of q, k, v and out); head_dim 64 or 128; any
+ * n_q_heads % n_kv_heads == 0.  Pointers must be 16-byte aligned.  Both
+ * products accumulate in fp32; the softmax weights enter the second one in
+ * `dtype` (their sum is taken in fp32, before that rounding).  No workspace.
+ * K and V must be finite within a sequence: a V value that is not reaches the
+ * rows that share its 128-key tile, also those before it.
+ */
+pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
+                            const int32_t* query_start_loc, float scale, int n_q_heads,
+                            int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            pa_dtype dtype, int32_t* dev_err, void* stream);
+
 /* ------------------------------------------------------------------------- */
 /* Slot write and copy-on-write block copy                                    */
 /* ------------------------------------------------------------------------- */
@@ -442,6 +534,39 @@ pa_status pa_swap_blocks(void* dst_k_pool, void* dst_v_pool, const void* src_k_p
                          int dst_num_blocks, pa_dtype kv_dtype, int32_t* dev_err,
                          void* stream);
 
+/*
+ * pa_compact_tokens -- after a tree of drafted tokens was checked
+ * (pa_decode_tree), move the K/V of the accepted path to the places right
+ * behind the prefix, in every layer's cache at once ([P1] §五: the accepted
+ * candidates are kept).  With n_s = tree_lens[s] and P_s = context_lens[s] -
+ * n_s, the row at position P_s + accepted[s][i] goes to position P_s + i for
+ * i < accepted_lens[s], every kv head, K and V; all as if every row were read
+ * before any is written.  The sequence then holds P_s + accepted_lens[s]
+ * tokens (pa_alloc_truncate); rows behind them are left as they are.
+ *
+ *   k_pools, v_pools  host arrays of n_layers device pools (see conventions)
+ *   tree_lens      device int32 [num_seqs], or NULL: all q_len
+ *   accepted       device int32 [num_seqs][max_accepted], strictly increasing
+ *                  node indices below n_s (a path of a tree whose parents come
+ *                  before their children is); entries from accepted_lens[s]
+ *                  on are not read
+ *   accepted_lens  device int32 [num_seqs], each in [0, max_accepted]
+ *   q_len          1 .. 64, the most nodes of a sequence
+ * The blocks that hold the tree must belong to their sequence alone
+ * (pa_alloc_prepare_write).  A sequence whose list breaks the rules above is
+ * left as it is and flagged: PA_DEVERR_SLOT for accepted or accepted_lens,
+ * PA_DEVERR_QUERY_LOC for tree_lens or a context shorter than its tree.  A
+ * move from or to a block id outside [0, num_blocks), or past the table, is
+ * left out and flagged with PA_DEVERR_BLOCK_ID.
+ */
+pa_status pa_compact_tokens(void* const* k_pools, void* const* v_pools, int n_layers,
+                            const int32_t* block_tables, const int32_t* context_lens,
+                            const int32_t* tree_lens, const int32_t* accepted,
+                            const int32_t* accepted_lens, int num_seqs, int q_len,
+                            int max_accepted, int max_blocks_per_seq, int n_kv_heads,
+                            int head_dim, int block_size, int num_blocks, pa_dtype kv_dtype,
+                            int32_t* dev_err, void* stream);
+
 /* ------------------------------------------------------------------------- */
 /* Host block allocator (not on the hot path)                                 */
 /* ------------------------------------------------------------------------- */
@@ -497,6 +622,18 @@ pa_status pa_alloc_fork(pa_alloc* a, int64_t parent, int64_t child);
  * *n_pairs_out is 0 or 1. */
 pa_status pa_alloc_prepare_write(pa_alloc* a, int64_t seq, int64_t* cow_pairs_out,
                                  int* n_pairs_out);
+
+/* Cut `seq` to its first n_tokens tokens (0 .. its length), e.g. to drop
+ * drafted tokens that were not accepted: blocks it no longer needs are
+ * released, last first, as pa_alloc_free_seq releases them; the sequence stays
+ * (with n_tokens 0 it holds no block).  `tokens` gives the ids of its last
+ * n_ids tokens, n_tokens - n_ids .. n_tokens - 1 (the accepted ones; n_ids 0:
+ * none, tokens may be NULL): when with them every token's id is known, the
+ * sequence registers full blocks again (prefix caching).  PA_ERR_INVALID_ARG
+ * for an unknown seq, n_tokens or n_ids out of range, or an id that differs
+ * from a known one. */
+pa_status pa_alloc_truncate(pa_alloc* a, int64_t seq, int n_tokens, const int32_t* tokens,
+                            int n_ids);
 
 /* Drop `seq`; each of its blocks' counts goes down by 1, last block first,
  * and a block whose count reaches 0 joins the back of the free queue (or,

@@ -32,7 +32,9 @@ EXPORTS = (
     "pa_decode_multi", "pa_alloc_set_prefix_caching", "pa_alloc_admit",
     "pa_alloc_append_tokens", "pa_alloc_cached_list", "pa_alloc_num_cached",
     "pa_swap_blocks", "pa_decode_shared_prefix", "pa_prefix_groups",
-    "pa_prefill_workspace_size", "pa_test_decode_timeout",
+    "pa_prefill_workspace_size", "pa_test_decode_timeout", "pa_decode_tree",
+    "pa_decode_tree_workspace_size", "pa_tree_masks", "pa_prefill_packed", "pa_compact_tokens",
+    "pa_alloc_truncate",
 )
 
 
@@ -92,12 +94,23 @@ def _load() -> ctypes.CDLL:
     L.pa_swap_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
     L.pa_decode_shared_prefix.argtypes = [P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, F, F,
                                           P, P, P, I, I, P, Z, P, P]
+    L.pa_decode_tree_workspace_size.argtypes = [I, I, I, I, I]
+    L.pa_decode_tree_workspace_size.restype = Z
+    L.pa_decode_tree.argtypes = [P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, F, F,
+                                 P, Z, P, P]
+    L.pa_tree_masks.argtypes = [P, P, I, I, P]
+    L.pa_prefill_packed.argtypes = [P, P, P, P, P, F, I, I, I, I, I, I64, I64, I64, I, P, P]
+    L.pa_compact_tokens.argtypes = [P, P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
+    L.pa_alloc_truncate.argtypes = [P, I64, I, P, I]
     L.pa_prefix_groups.argtypes = [P, P, I, I, I, I, I, P, P, P, P, P]
     L.pa_alloc_set_prefix_caching.argtypes = [P, I]
     L.pa_alloc_admit.argtypes = [P, I64, P, I, P, P]
     L.pa_alloc_append_tokens.argtypes = [P, I64, P, I, P]
     L.pa_alloc_cached_list.argtypes = [P, P, I, P]
     L.pa_alloc_num_cached.argtypes = [P]
+    for fn in ("pa_decode_tree", "pa_tree_masks", "pa_prefill_packed", "pa_compact_tokens",
+               "pa_alloc_truncate"):
+        getattr(L, fn).restype = I
     for fn in ("pa_alloc_num_tokens", "pa_alloc_refcount", "pa_alloc_num_free",
                "pa_alloc_num_seqs", "pa_alloc_num_cached"):
         getattr(L, fn).restype = I
@@ -134,6 +147,30 @@ def _stream(stream, device) -> ctypes.c_void_p:
 def _check(status: int, what: str):
     if status != PA_OK:
         raise PAError(status, what)
+
+
+def _on_device(ref, *ts):
+    """Every tensor of a call lives on `ref`'s CUDA device."""
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise PAError(PA_ERR_INVALID_ARG, f"a tensor is on {t.device}, not {ref.device}")
+    if ref.device.type != "cuda":
+        raise PAError(PA_ERR_INVALID_ARG, "tensors must be on a CUDA device")
+
+
+class _current:
+    """Makes `device` the current one for a launch (its stream's device)."""
+
+    def __init__(self, device):
+        self._to, self._was = device.index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self._to != self._was:
+            torch.cuda.set_device(self._to)
+
+    def __exit__(self, *exc):
+        if self._to != self._was:
+            torch.cuda.set_device(self._was)
 
 
 def _contig(*ts):
@@ -193,6 +230,71 @@ def pa_decode_multi(out, q, k_pool, v_pool, block_tables, context_lens, scale, k
                                mb, num_blocks, dtype_code(q), dtype_code(k_pool), float(k_scale),
                                float(v_scale), _p(workspace), ws_bytes, _p(dev_err),
                                _stream(stream, q.device)), "pa_decode_multi")
+    return out
+
+
+def pa_decode_tree_workspace_size(num_seqs: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                  head_dim: int) -> int:
+    return lib.pa_decode_tree_workspace_size(num_seqs, q_len, n_q_heads, n_kv_heads, head_dim)
+
+
+def alloc_tree_workspace(q: torch.Tensor, k_pool: torch.Tensor) -> torch.Tensor:
+    """Workspace for pa_decode_tree with these queries and this cache; calls
+    that may overlap (other streams, captured graphs) need one each."""
+    n = pa_decode_tree_workspace_size(q.shape[0], q.shape[1], q.shape[2], k_pool.shape[1],
+                                      q.shape[3])
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def tree_masks(parents: torch.Tensor, tree_lens=None) -> torch.Tensor:
+    """The masks pa_decode_tree takes, of trees given by their parents
+    ([num_seqs, q_len], -1 for a node that continues the prefix; from host
+    copies): an int64 CPU tensor [num_seqs, q_len], bit j of row i set where
+    node j is node i or one of its ancestors."""
+    if parents.dim() != 2:
+        raise PAError(PA_ERR_INVALID_ARG, "tree_masks: parents must be [num_seqs, q_len]")
+    par = parents.detach().cpu().contiguous().to(torch.int32)
+    lens = None
+    if tree_lens is not None:
+        lens = tree_lens.detach().cpu().contiguous().to(torch.int32)
+        if tuple(lens.shape) != (par.shape[0],):
+            raise PAError(PA_ERR_INVALID_ARG, "tree_masks: tree_lens must be [num_seqs]")
+    out = torch.zeros(par.shape, dtype=torch.int64)
+    _check(lib.pa_tree_masks(_p(par), _p(lens), par.shape[0], par.shape[1], _p(out)),
+           "pa_tree_masks")
+    return out
+
+
+def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, scale,
+                   tree_lens=None, k_scale=1.0, v_scale=1.0, workspace=None, dev_err=None,
+                   stream=None):
+    """Tree decode: q / out are [num_seqs, q_len, n_q, d]; node i of sequence s
+    attends to the context before the tree and to the nodes j whose bit is set
+    in masks[s, i] (int64, see tree_masks)."""
+    _contig(out, q, k_pool, v_pool, block_tables, context_lens, masks, tree_lens, workspace)
+    _on_device(q, out, k_pool, v_pool, block_tables, context_lens, masks, tree_lens, workspace,
+               dev_err)
+    num_seqs, q_len, n_q, d = q.shape
+    num_blocks, n_kv, bs, d2 = k_pool.shape
+    if d2 != d or v_pool.shape != k_pool.shape or out.shape != q.shape or \
+            masks.shape != q.shape[:2] or block_tables.shape[0] != num_seqs or \
+            context_lens.shape != q.shape[:1] or \
+            (tree_lens is not None and tree_lens.shape != q.shape[:1]):
+        raise PAError(PA_ERR_INVALID_ARG, "pa_decode_tree shapes")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or \
+            (tree_lens is not None and tree_lens.dtype != torch.int32):
+        raise PAError(PA_ERR_INVALID_ARG, "block_tables / context_lens / tree_lens must be int32")
+    if masks.dtype != torch.int64 or out.dtype != q.dtype or v_pool.dtype != k_pool.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_decode_tree dtypes")
+    if workspace is None:
+        workspace = alloc_tree_workspace(q, k_pool)
+    with _current(q.device):
+        _check(lib.pa_decode_tree(
+            _p(out), _p(q), _p(k_pool), _p(v_pool), _p(block_tables), _p(context_lens), _p(masks),
+            _p(tree_lens), float(scale), bs, n_q, n_kv, d, num_seqs, q_len,
+            block_tables.shape[1], num_blocks, dtype_code(q), dtype_code(k_pool), float(k_scale),
+            float(v_scale), _p(workspace), workspace.numel() * workspace.element_size(),
+            _p(dev_err), _stream(stream, q.device)), "pa_decode_tree")
     return out
 
 
@@ -335,6 +437,37 @@ def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, query_start_loc, cont
     return out
 
 
+def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream=None):
+    """Causal attention over whole prompts lying one behind another: q / out are
+    [total, n_q, d], k / v [total, n_kv, d]; sequence s owns rows
+    query_start_loc[s] .. query_start_loc[s + 1] - 1 (int32, on the device).
+    q, k and v may be strided along the tokens (parts of one projection)."""
+    _contig(out, query_start_loc)
+    _on_device(q, out, k, v, query_start_loc, dev_err)
+    total, n_q, d = q.shape
+    n_kv = k.shape[1]
+    if out.shape != q.shape or k.shape != (total, n_kv, d) or v.shape != k.shape or \
+            query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_prefill_packed shapes")
+    if query_start_loc.dtype != torch.int32:
+        raise PAError(PA_ERR_INVALID_ARG, "query_start_loc must be int32")
+    if not out.dtype == q.dtype == k.dtype == v.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_prefill_packed dtypes")
+    strides = []
+    for t in (q, k, v):
+        st = t.stride()
+        if st[2] != 1 and d > 1 or st[1] != d and t.shape[1] > 1:
+            raise PAError(PA_ERR_INVALID_ARG, "a token's heads must be contiguous")
+        # a single token's stride is never used
+        strides.append(st[0] if total > 1 else t.shape[1] * d)
+    with _current(q.device):
+        _check(lib.pa_prefill_packed(_p(out), _p(q), _p(k), _p(v), _p(query_start_loc),
+                                     float(scale), n_q, n_kv, d, query_start_loc.shape[0] - 1,
+                                     total, *strides, dtype_code(q), _p(dev_err),
+                                     _stream(stream, q.device)), "pa_prefill_packed")
+    return out
+
+
 # --------------------------------------------------------------------------
 # slot write / block copy
 # --------------------------------------------------------------------------
@@ -383,6 +516,57 @@ def pa_swap_blocks(dst_k, dst_v, src_k, src_v, block_pairs, dev_err=None, stream
                               _p(dev_err), _stream(stream, dev)), "pa_swap_blocks")
 
 
+def _pool_pointers(pools):
+    """(array of pool pointers, layers, one layer's shape, dtype, device) of a
+    list of per-layer pools or one [n_layers, ...] tensor."""
+    if isinstance(pools, torch.Tensor):
+        if pools.dim() != 5 or (pools.shape[0] and not pools[0].is_contiguous()):
+            raise PAError(PA_ERR_INVALID_ARG, "pools must be [n_layers, num_blocks, n_kv, 16, d], "
+                                              "each layer contiguous")
+        n, base, step = pools.shape[0], pools.data_ptr(), pools.stride(0) * pools.element_size()
+        return (ctypes.c_void_p * max(n, 1))(*[base + i * step for i in range(n)]), n, \
+            pools.shape[1:], pools
+    _contig(*pools)
+    for t in pools:
+        if t.shape != pools[0].shape or t.dtype != pools[0].dtype or t.dim() != 4:
+            raise PAError(PA_ERR_INVALID_ARG, "every layer's pool must have the same shape")
+        _on_device(pools[0], t)
+    return (ctypes.c_void_p * max(len(pools), 1))(*[t.data_ptr() for t in pools]), len(pools), \
+        pools[0].shape if pools else None, pools[0] if pools else None
+
+
+def pa_compact_tokens(k_pools, v_pools, block_tables, context_lens, tree_lens, accepted,
+                      accepted_lens, q_len=64, dev_err=None, stream=None):
+    """Moves the accepted tokens' K/V rows (accepted [num_seqs, max_accepted],
+    strictly increasing tree nodes; accepted_lens [num_seqs]) to the positions
+    right behind the prefix, in every layer.  k_pools / v_pools: lists of the
+    layers' pools, or tensors [n_layers, num_blocks, n_kv, 16, d].  tree_lens
+    None: every tree has q_len nodes."""
+    kp, n_layers, shape, kt = _pool_pointers(k_pools)
+    vp, n_v, v_shape, vt = _pool_pointers(v_pools)
+    if n_layers != n_v or shape != v_shape:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens pool shapes")
+    if n_layers == 0:
+        return
+    ints = (block_tables, context_lens, accepted, accepted_lens) + \
+        (() if tree_lens is None else (tree_lens,))
+    _contig(*ints)
+    _on_device(kt, vt, dev_err, *ints)
+    if any(t.dtype != torch.int32 for t in ints) or kt.dtype != vt.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens dtypes (index tensors: int32)")
+    num_seqs, max_accepted = accepted.shape
+    if block_tables.shape[0] != num_seqs or any(
+            t.shape != (num_seqs,) for t in (context_lens, accepted_lens) + ints[4:]):
+        raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens shapes")
+    num_blocks, n_kv, bs, d = shape
+    with _current(kt.device):
+        _check(lib.pa_compact_tokens(kp, vp, n_layers, _p(block_tables), _p(context_lens),
+                                     _p(tree_lens), _p(accepted), _p(accepted_lens), num_seqs,
+                                     int(q_len), max_accepted, block_tables.shape[1], n_kv, d, bs,
+                                     num_blocks, dtype_code(kt), _p(dev_err),
+                                     _stream(stream, kt.device)), "pa_compact_tokens")
+
+
 # --------------------------------------------------------------------------
 # host allocator
 # --------------------------------------------------------------------------
@@ -425,6 +609,12 @@ class BlockAllocator:
 
     def free_seq(self, seq: int) -> int:
         return lib.pa_alloc_free_seq(self._h, seq)
+
+    def truncate(self, seq: int, n_tokens: int, tokens=()) -> int:
+        """Cut seq to n_tokens tokens; tokens: the ids of its last ones."""
+        toks = (ctypes.c_int32 * max(len(tokens), 1))(*tokens)
+        return lib.pa_alloc_truncate(self._h, seq, n_tokens, ctypes.cast(toks, ctypes.c_void_p),
+                                     len(tokens))
 
     def block_table(self, seq: int):
         cap = self.num_blocks

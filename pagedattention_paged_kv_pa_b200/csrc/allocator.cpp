@@ -44,8 +44,8 @@ struct Seq {
   std::vector<int32_t> blocks;  // physical ids, logical order
   int64_t n_tokens = 0;
   bool known = true;             // every token id of the sequence is known
-  std::vector<int32_t> tokens;   // the ids, while known
-  std::vector<uint64_t> hchain;  // prefix hash of each full block, while known
+  std::vector<int32_t> tokens;   // the ids of its known leading tokens (all, while known)
+  std::vector<uint64_t> hchain;  // prefix hash of each full block of them
 };
 
 // 64-bit mix (the splitmix64 finaliser)
@@ -138,6 +138,18 @@ struct pa_alloc {
     }
   }
 
+  // one sequence less holds block b; at zero it is free: cached if it is
+  // registered, else empty
+  void release(int32_t b) {
+    if (--rc[b] != 0) return;
+    if (reg[b]) {
+      lru.push_back(b);
+      lru_pos[b] = std::prev(lru.end());
+    } else {
+      free_q.push_back(b);
+    }
+  }
+
   // reserve slots for n new tokens of seq (creating it), all-or-nothing
   pa_status append(int64_t seq, int n_tokens, int64_t* slots_out) {
     const int64_t B = block_size;
@@ -149,6 +161,8 @@ struct pa_alloc {
     const int64_t need = (n + n_tokens + B - 1) / B - have;
     if (need > (int64_t)allocatable()) return PA_ERR_OOM;
     Seq& s = seqs[seq];  // creates the sequence on first use
+    // a registered last block that was cut (pa_alloc_truncate) is written again
+    if (n_tokens > 0 && n % B != 0 && reg[s.blocks.back()]) unregister(s.blocks.back());
     for (int64_t i = 0; i < need; i++) s.blocks.push_back(take());
     for (int64_t p = n; p < n + n_tokens; p++)
       slots_out[p - n] = (int64_t)s.blocks[p / B] * B + p % B;
@@ -207,11 +221,9 @@ pa_status pa_alloc_append(pa_alloc* a, int64_t seq, int n_tokens, int64_t* slots
   pa_status st = a->append(seq, n_tokens, slots_out);
   if (st != PA_OK) return st;
   Seq& s = a->seqs[seq];
-  if (n_tokens > 0 || is_new) {  // tokens without ids: no longer known
-    s.known = false;
-    s.tokens.clear();
-    s.hchain.clear();
-  }
+  // tokens without ids: no longer known (the ids of the tokens before them
+  // stay, for pa_alloc_truncate)
+  if (n_tokens > 0 || is_new) s.known = false;
   return PA_OK;
 }
 
@@ -304,18 +316,39 @@ pa_status pa_alloc_free_seq(pa_alloc* a, int64_t seq) {
   auto it = a->seqs.find(seq);
   if (it == a->seqs.end()) return PA_ERR_INVALID_ARG;
   const auto& bl = it->second.blocks;
-  for (size_t k = bl.size(); k-- > 0;) {  // last block first
-    const int32_t b = bl[k];
-    if (--a->rc[b] == 0) {
-      if (a->reg[b]) {
-        a->lru.push_back(b);
-        a->lru_pos[b] = std::prev(a->lru.end());
-      } else {
-        a->free_q.push_back(b);
-      }
-    }
-  }
+  for (size_t k = bl.size(); k-- > 0;) a->release(bl[k]);  // last block first
   a->seqs.erase(it);
+  return PA_OK;
+}
+
+pa_status pa_alloc_truncate(pa_alloc* a, int64_t seq, int n_tokens, const int32_t* tokens,
+                            int n_ids) {
+  if (!a || n_tokens < 0 || n_ids < 0 || n_ids > n_tokens || (n_ids > 0 && !tokens))
+    return PA_ERR_INVALID_ARG;
+  auto it = a->seqs.find(seq);
+  if (it == a->seqs.end() || n_tokens > it->second.n_tokens) return PA_ERR_INVALID_ARG;
+  Seq& s = it->second;
+  const size_t n = (size_t)n_tokens, first = n - (size_t)n_ids;
+  // ids given again must agree with the ones known, whose blocks may be shared
+  for (size_t i = first; i < n && i < s.tokens.size(); i++)
+    if (tokens[i - first] != s.tokens[i]) return PA_ERR_INVALID_ARG;
+  const bool more = first <= s.tokens.size() && s.tokens.size() < n;
+  try {  // whatever can fail, before anything changes
+    if (more) s.tokens.reserve(n);
+  } catch (...) {
+    return PA_ERR_OOM;
+  }
+  if (more) s.tokens.insert(s.tokens.end(), tokens + (s.tokens.size() - first), tokens + n_ids);
+  if (s.tokens.size() > n) s.tokens.resize(n);
+  if (s.hchain.size() > n / kB) s.hchain.resize(n / kB);
+  const size_t keep = (n + kB - 1) / kB;
+  while (s.blocks.size() > keep) {  // last block first
+    a->release(s.blocks.back());
+    s.blocks.pop_back();
+  }
+  s.n_tokens = n_tokens;
+  s.known = s.tokens.size() == n;
+  a->register_full(s, 0);
   return PA_OK;
 }
 

@@ -9,6 +9,7 @@
 
 #include "mq_tc.h"
 #include "pa_internal.h"
+#include "serve_ops.h"
 
 namespace {
 
@@ -446,6 +447,84 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
                             workspace_bytes, stream);
 }
 
+size_t pa_decode_tree_workspace_size(int num_seqs, int q_len, int n_q_heads, int n_kv_heads,
+                                     int head_dim) {
+  (void)num_seqs, (void)q_len, (void)n_q_heads, (void)n_kv_heads, (void)head_dim;
+  return 0;
+}
+
+pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* context_lens,
+                         const uint64_t* masks, const int32_t* tree_lens, float scale,
+                         int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                         int num_seqs, int q_len, int max_blocks_per_seq, int num_blocks,
+                         pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale, float v_scale,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                         void* stream) {
+  const DecodeShape s{n_q_heads, n_kv_heads, head_dim, num_seqs, max_blocks_per_seq, num_blocks, 1};
+  const pa_status st = check_decode(s, block_size, q_dtype, kv_dtype);
+  if (st != PA_OK) return st;
+  if (q_len < 1 || q_len > 64) return PA_ERR_INVALID_ARG;
+  if (q_dtype == PA_F32) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * q_len * n_q_heads >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens || !masks)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) ||
+      (reinterpret_cast<uintptr_t>(masks) & 7u))
+    return PA_ERR_INVALID_ARG;
+  const bool fp8 = kv_dtype == PA_FP8_E4M3;
+  if (!(scale == scale) || (fp8 && !(k_scale > 0.f && v_scale > 0.f))) return PA_ERR_INVALID_ARG;
+  const size_t need =
+      pa_decode_tree_workspace_size(num_seqs, q_len, n_q_heads, n_kv_heads, head_dim);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return PA_ERR_INVALID_ARG;
+  pa::TreeParams p;
+  p.out = out;
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.tree_lens = tree_lens;
+  p.masks = masks;
+  p.dev_err = dev_err;
+  p.scale_log2 = scale * kLog2e * (fp8 ? k_scale : 1.f);
+  p.out_mul = fp8 ? v_scale : 1.f;
+  p.n_q = n_q_heads;
+  p.n_kv = n_kv_heads;
+  p.group = n_q_heads / n_kv_heads;
+  p.num_seqs = num_seqs;
+  p.q_len = q_len;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  return cuda_status(pa::launch_tree(p, head_dim, q_dtype == PA_BF16, fp8,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_tree_masks(const int32_t* parents, const int32_t* tree_lens, int num_seqs,
+                        int q_len, uint64_t* masks_out) {
+  if (num_seqs < 0 || q_len < 1 || q_len > 64) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!parents || !masks_out) return PA_ERR_INVALID_ARG;
+  const auto nodes = [&](int s) { return tree_lens ? tree_lens[s] : q_len; };
+  for (int s = 0; s < num_seqs; s++) {
+    if (nodes(s) < 0 || nodes(s) > q_len) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < nodes(s); i++) {
+      const int up = parents[(size_t)s * q_len + i];
+      if (up < -1 || up >= i) return PA_ERR_INVALID_ARG;
+    }
+  }
+  for (int s = 0; s < num_seqs; s++) {
+    uint64_t* m = masks_out + (size_t)s * q_len;
+    for (int i = 0; i < q_len; i++) {
+      const int up = i < nodes(s) ? parents[(size_t)s * q_len + i] : -1;
+      m[i] = i < nodes(s) ? (uint64_t(1) << i) | (up >= 0 ? m[up] : 0) : 0;
+    }
+  }
+  return PA_OK;
+}
+
 pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_pool,
                                   const void* v_pool, const int32_t* block_tables,
                                   const int32_t* context_lens, float scale, int block_size,
@@ -638,6 +717,47 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
                                         static_cast<cudaStream_t>(stream)));
 }
 
+pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
+                            const int32_t* query_start_loc, float scale, int n_q_heads,
+                            int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            pa_dtype dtype, int32_t* dev_err, void* stream) {
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || total_tokens < 0 || !valid_dtype(dtype)) return PA_ERR_INVALID_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (n_q_heads > 65535 || num_seqs > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (!(scale == scale)) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_tokens == 0) return PA_OK;
+  if (!out || !q || !k || !v || !query_start_loc) return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+    return PA_ERR_INVALID_ARG;
+  const int64_t qn = (int64_t)n_q_heads * head_dim, kn = (int64_t)n_kv_heads * head_dim;
+  if (q_stride < qn || k_stride < kn || v_stride < kn ||
+      ((q_stride | k_stride | v_stride) & 7) != 0)
+    return PA_ERR_INVALID_ARG;
+  // the tensor maps' strides are 40 bits of bytes
+  if (std::max({q_stride, k_stride, v_stride}) >= (int64_t(1) << 38)) return PA_ERR_UNSUPPORTED;
+  pa::PromptParams p;
+  p.out = out;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.query_start_loc = query_start_loc;
+  p.dev_err = dev_err;
+  p.scale_log2 = scale * kLog2e;
+  p.n_q = n_q_heads;
+  p.n_kv = n_kv_heads;
+  p.group = n_q_heads / n_kv_heads;
+  p.num_seqs = num_seqs;
+  p.total = total_tokens;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  return cuda_status(
+      pa::launch_prompt(p, head_dim, dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
 pa_status pa_reshape_and_cache(void* k_pool, void* v_pool, const void* key, const void* value,
                                const int64_t* slot_mapping, int num_tokens, int n_kv_heads,
                                int head_dim, int block_size, int num_blocks, pa_dtype src_dtype,
@@ -744,6 +864,55 @@ pa_status pa_swap_blocks(void* dst_k_pool, void* dst_v_pool, const void* src_k_p
   p.dst_num_blocks = dst_num_blocks;
   p.block_bytes = bb;
   return cuda_status(pa::launch_copy_blocks(p, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_compact_tokens(void* const* k_pools, void* const* v_pools, int n_layers,
+                            const int32_t* block_tables, const int32_t* context_lens,
+                            const int32_t* tree_lens, const int32_t* accepted,
+                            const int32_t* accepted_lens, int num_seqs, int q_len,
+                            int max_accepted, int max_blocks_per_seq, int n_kv_heads,
+                            int head_dim, int block_size, int num_blocks, pa_dtype kv_dtype,
+                            int32_t* dev_err, void* stream) {
+  if (block_size != 16) return PA_ERR_UNSUPPORTED;
+  if (n_layers < 0 || num_seqs < 0 || max_accepted < 0 || max_blocks_per_seq < 1 ||
+      n_kv_heads < 1 || head_dim < 1 || num_blocks < 1 || !valid_dtype(kv_dtype))
+    return PA_ERR_INVALID_ARG;
+  if (q_len < 1 || q_len > 64) return PA_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)head_dim * elem_bytes(kv_dtype);
+  if (row % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)n_kv_heads * (row / 16) * 2 * pa::kCompactLayers >= (int64_t(1) << 31))
+    return PA_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * 16 >= (int64_t(1) << 30)) return PA_ERR_UNSUPPORTED;
+  if (n_layers == 0 || num_seqs == 0 || max_accepted == 0) return PA_OK;
+  if (!k_pools || !v_pools || !block_tables || !context_lens || !accepted || !accepted_lens)
+    return PA_ERR_INVALID_ARG;
+  for (int l = 0; l < n_layers; l++)
+    if (!k_pools[l] || !v_pools[l] || !aligned16(k_pools[l]) || !aligned16(v_pools[l]))
+      return PA_ERR_INVALID_ARG;
+  pa::CompactParams p;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.tree_lens = tree_lens;
+  p.accepted = accepted;
+  p.accepted_lens = accepted_lens;
+  p.dev_err = dev_err;
+  p.num_seqs = num_seqs;
+  p.q_len = q_len;
+  p.max_accepted = max_accepted;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.n_kv = n_kv_heads;
+  p.chunks = static_cast<int>(row / 16);
+  for (int l0 = 0; l0 < n_layers; l0 += pa::kCompactLayers) {
+    p.n_layers = std::min(n_layers - l0, pa::kCompactLayers);
+    for (int l = 0; l < p.n_layers; l++) {
+      p.pools[2 * l] = k_pools[l0 + l];
+      p.pools[2 * l + 1] = v_pools[l0 + l];
+    }
+    const cudaError_t e = pa::launch_compact(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return PA_OK;
 }
 
 }  // extern "C"

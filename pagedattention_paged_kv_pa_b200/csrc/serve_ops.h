@@ -1,0 +1,52 @@
+// Launchers of the steps around decode -- whole-prompt attention, attention of
+// a tree of drafted tokens, moving the accepted tokens' K/V -- that the C ABI
+// shim calls.  Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/pa.h"
+
+namespace pa {
+
+// Whole-prompt attention: sequence s owns rows query_start_loc[s] ..
+// query_start_loc[s + 1] - 1 of q, k, v and out.
+struct PromptParams {
+  void* out;  // [total][n_q][D]
+  const void *q, *k, *v;
+  const int32_t* query_start_loc;
+  int32_t* dev_err;
+  float scale_log2;  // scale x log2(e)
+  int n_q, n_kv, group, num_seqs, total;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+};
+cudaError_t launch_prompt(const PromptParams& p, int D, bool bf16, cudaStream_t st);
+
+// Attention of a tree of drafted tokens over the paged cache.
+struct TreeParams {
+  void* out;  // [num_seqs][q_len][n_q][D]
+  const void *q, *k_pool, *v_pool;
+  const int32_t *block_tables, *context_lens, *tree_lens;
+  const uint64_t* masks;  // [num_seqs][q_len]
+  int32_t* dev_err;
+  float scale_log2;  // scale x log2(e) (x k_scale for fp8 caches)
+  float out_mul;     // v_scale for fp8 caches, else 1
+  int n_q, n_kv, group, num_seqs, q_len, max_blocks, num_blocks;
+};
+cudaError_t launch_tree(const TreeParams& p, int D, bool bf16, bool fp8, cudaStream_t st);
+
+// Moving the accepted tokens' rows, all layers of a launch at once.
+constexpr int kCompactLayers = 64;  // layers per launch (pointers travel as arguments)
+struct CompactParams {
+  void* pools[2 * kCompactLayers];  // k_pool, v_pool of each layer
+  const int32_t *block_tables, *context_lens, *tree_lens, *accepted, *accepted_lens;
+  int32_t* dev_err;
+  int n_layers, num_seqs, q_len, max_accepted, max_blocks, num_blocks, n_kv;
+  int chunks;  // 16-byte pieces of a row of one kv head
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
+
+}  // namespace pa
