@@ -1,0 +1,156 @@
+// The softmax of one row of a 128-row attention tile by one thread: scores
+// come from TMEM (S = Q K^T, fp32), the weights go back over them as 16-bit
+// pairs, the A operand of O += P V.
+//
+// With the scores in log2 units (s = scale log2(e) q . k) the thread keeps the
+// maximum m it has exponentiated against and the sum l of 2^(s - m); O in TMEM
+// holds the sum of 2^(s - m) v.  When the row's maximum grows by more than
+// kRescaleLog2, l and O are multiplied by 2^(m - m') and m becomes m'; up to
+// there the weights may exceed 1 by that factor, which fp32 sums and 16-bit
+// weights (f16 up to 65504) hold.
+//
+// What bounds it is the exponential: 16 a clock and SM on the special-function
+// unit, i.e. 1024 clocks for a 128 x 128 tile, as long as the two products of
+// a 128-wide head take on the tensor cores.  Part of the exponentials of tiles
+// without a mask therefore runs on the FMA pipe (exp2_poly2).
+#pragma once
+
+#include "tc_ops.cuh"
+
+namespace pa {
+namespace attn {
+
+constexpr int kTileM = 128;           // rows of a tile: one per TMEM lane
+constexpr int kTileN = 128;           // keys per tile
+constexpr float kRescaleLog2 = 8.f;   // lazy rescale threshold (factor 256)
+
+// ------------------------------------------------- two fp32 values at a time
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (the
+// low bits of x + 1.5 2^23) and f in [-1/2, 1/2]; a degree-3 polynomial with
+// the smallest largest relative error on that interval (2^-13.7, below half a
+// step of f16) gives 2^f, and n is added to its exponent field.  x below -126
+// gives 2^-126 instead of less, so that the exponent field cannot wrap.
+__device__ __forceinline__ void exp2_poly2(float& a, float& b) {
+  const uint64_t x = f2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t t = add2(x, f2(12582912.f, 12582912.f));
+  const uint64_t n = add2(t, f2(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(n, f2(-1.f, -1.f), x);
+  uint64_t p = fma2(f, f2(0.0551716685295105f, 0.0551716685295105f),
+                    f2(0.2426111251115799f, 0.2426111251115799f));
+  p = fma2(p, f, f2(0.6932609677314758f, 0.6932609677314758f));
+  p = fma2(p, f, f2(0.9999280571937561f, 0.9999280571937561f));
+  float ta, tb, pa, pb;
+  un2(t, ta, tb);
+  un2(p, pa, pb);
+  a = __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
+  b = __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
+}
+
+struct RowState {
+  float m, l;  // maximum exponentiated against (log2 units), sum of the weights
+};
+
+// bits of keys first .. first + 31 that are at or below the last visible key
+__device__ __forceinline__ uint32_t bits_upto(int first, int last) {
+  const int n = last - first + 1;
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// The row's scores of a tile: 128 columns of S at `ts` (this warp's lanes).
+__device__ __forceinline__ void load_scores(uint32_t ts, float (&x)[kTileN]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+  for (int c = 0; c < kTileN; c += 32) tc::ld32x32b_x32(ts + c, r + c);
+  tc::wait_ld();
+}
+
+// Largest score of the row in log2 units; with a mask (full false) x becomes
+// the scores in log2 units, -inf where vis has no bit.
+__device__ __forceinline__ float tile_max(float (&x)[kTileN], bool full, const uint32_t (&vis)[4],
+                                          float sl) {
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (full) {
+#pragma unroll
+    for (int e = 0; e < kTileN; e += 8)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(x[e + 2 * c], x[e + 2 * c + 1]));
+    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+  }
+#pragma unroll
+  for (int e = 0; e < kTileN; ++e) {
+    x[e] = (vis[e >> 5] >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
+    m4[e & 3] = fmaxf(m4[e & 3], x[e]);
+  }
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+}
+
+// Multiplies `cols` columns of the row's O by alpha.
+__device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t o[32];
+    tc::ld32x32b_x32(to + c, o);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tc::st32x32b_x32(to + c, o);
+  }
+  tc::wait_st();
+}
+
+// Weights of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns their
+// fp32 sum.  Of every 8 pairs without a mask kPoly go through exp2_poly2.
+template <bool BF16, int kPoly>
+__device__ __forceinline__ float tile_weights(const float (&x)[kTileN], int h, bool full, float sl,
+                                              float neg_m, uint32_t (&pk)[32]) {
+  uint64_t s[2] = {0ull, 0ull};
+  const uint64_t nm = f2(neg_m, neg_m), s2 = f2(sl, sl);
+  if (full) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      float a, b;
+      un2(fma2(f2(x[64 * h + 2 * c], x[64 * h + 2 * c + 1]), s2, nm), a, b);
+      if ((c & 7) < kPoly) {
+        exp2_poly2(a, b);
+      } else {
+        a = tc::ex2(a);
+        b = tc::ex2(b);
+      }
+      s[c & 1] = add2(s[c & 1], f2(a, b));
+      pk[c] = pack2<BF16>(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const float a = tc::ex2(x[64 * h + 2 * c] + neg_m);
+      const float b = tc::ex2(x[64 * h + 2 * c + 1] + neg_m);
+      s[c & 1] = add2(s[c & 1], f2(a, b));
+      pk[c] = pack2<BF16>(a, b);
+    }
+  }
+  float a, b;
+  un2(add2(s[0], s[1]), a, b);
+  return a + b;
+}
+
+}  // namespace attn
+}  // namespace pa

@@ -11,6 +11,23 @@
 #include "pa_internal.h"
 #include "serve_ops.h"
 
+namespace pa {
+
+int device_sms() {
+  static int n[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (n[dev] == 0) {
+    int v = 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1)
+      v = 148;
+    n[dev] = v;
+  }
+  return n[dev];
+}
+
+}  // namespace pa
+
 namespace {
 
 using pa::DecodeParams;
@@ -131,6 +148,25 @@ bool q_rows_map(const void* q, int rows, int n_q, int group, int q_len, CUtensor
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(q_len)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map over 16-bit rows [tokens][heads][d] with `stride` elements between tokens:
+// one box is 64 columns of `box_h` heads of `box_t` tokens, written as rows
+// token x box_h + head with the 128-byte swizzle; rows past the last token read
+// as zeros.  Not cached: these tensors change from call to call.
+bool tokens_map(const void* x, int tokens, int heads, int d, int64_t stride, int box_h, int box_t,
+                CUtensorMap* m) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_h), static_cast<cuuint32_t>(box_t)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(x), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -740,9 +776,6 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
   if (std::max({q_stride, k_stride, v_stride}) >= (int64_t(1) << 38)) return PA_ERR_UNSUPPORTED;
   pa::PromptParams p;
   p.out = out;
-  p.q = q;
-  p.k = k;
-  p.v = v;
   p.query_start_loc = query_start_loc;
   p.dev_err = dev_err;
   p.scale_log2 = scale * kLog2e;
@@ -751,11 +784,16 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
   p.group = n_q_heads / n_kv_heads;
   p.num_seqs = num_seqs;
   p.total = total_tokens;
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  return cuda_status(
-      pa::launch_prompt(p, head_dim, dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
+  p.log2_hb = 0;
+  while (p.log2_hb < 4 && p.group % (2 << p.log2_hb) == 0) ++p.log2_hb;
+  CUtensorMap tmq, tmk, tmv;
+  const int hb = 1 << p.log2_hb;
+  if (!tokens_map(q, total_tokens, n_q_heads, head_dim, q_stride, hb, 128 / hb, &tmq) ||
+      !tokens_map(k, total_tokens, n_kv_heads, head_dim, k_stride, 1, 128, &tmk) ||
+      !tokens_map(v, total_tokens, n_kv_heads, head_dim, v_stride, 1, 128, &tmv))
+    return PA_ERR_CUDA;
+  return cuda_status(pa::launch_prompt(p, head_dim, dtype == PA_BF16, &tmq, &tmk, &tmv,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_reshape_and_cache(void* k_pool, void* v_pool, const void* key, const void* value,

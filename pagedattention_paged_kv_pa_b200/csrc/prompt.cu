@@ -1,50 +1,526 @@
-// Whole-prompt attention (pa_prefill_packed): one warp per (token, head).
-#include "attn_rows.cuh"
+// Whole-prompt attention (pa_prefill_packed) on tcgen05 tensor cores.
+//
+// out[r][h] = sum over keys u <= r of r's sequence of 2^(s_u - m) v_u / l, with
+// s = scale log2(e) q . k, m the row's maximum and l the sum of the weights:
+// one pass over the keys with the running (m, l) of attn_tile.cuh.
+//
+// Tiles.  A 128-row tile is HB query heads of one kv head (HB: the power of
+// two in the group size, at most 16) times QT = 128 / HB consecutive queries,
+// row r = query r / HB, head r % HB; so each K/V tile of 128 keys serves HB
+// heads and every group size fills its tiles.  An item of work is two such
+// tiles, A and B, one behind the other in the sequence, over the same keys: the
+// tensor cores work on one while the softmax of the other runs.  TMEM holds S
+// of A and B (128 fp32 columns each; P goes over S as 16-bit pairs) and O of
+// A and B.
+//
+// Persistent CTAs, one per SM.  The items are ordered by their position in
+// their sequence, the last ones (which see the most keys) first, over all
+// sequences together, so the CTAs, which take them in turn there and back,
+// end at about the same time: a scheduler warp walks that order from the
+// sequence starts alone (no list in memory, no order of arrival), ahead of the
+// other warps.
+//
+// Roles: warps 0-3 softmax of tile A, warps 4-7 of tile B (one thread per
+// row, its 128 scores in registers), warp 8 owns TMEM and issues the MMAs,
+// warp 9 loads Q, K and V by TMA (K and V share a ring of stages), warp 10
+// schedules, warp 11 zeroes the rows of an item's last V tile that lie behind
+// its sequence (another sequence's values or padding: 0 x NaN must not reach
+// O).  Every wait is bounded; a role that gives up flags PA_DEVERR_TIMEOUT and
+// leaves, and the CTA drains its loads and MMAs and frees TMEM.
+#include <type_traits>
+
+#include "attn_tile.cuh"
 #include "serve_ops.h"
 
 namespace pa {
 
 namespace {
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptParams p) {
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x >> 5;
-  const long long rows = (long long)p.total * p.n_q;
-  for (long long i = blockIdx.x * 4ll + warp; i < rows; i += gridDim.x * 4ll) {
-    const int h = (int)(i % p.n_q), t = (int)(i / p.n_q);
-    // the sequence that owns row t (the last one whose start is at or before it)
-    for (int s = 0; s < p.num_seqs; ++s) {
-      const int a = p.query_start_loc[s], b = min(p.query_start_loc[s + 1], p.total);
-      if (a < 0 || b < a) {
-        if (i == 0) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
-        continue;
+using attn::kTileM;
+using attn::kTileN;
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11: see the roles
+constexpr int kItems = 4;              // items scheduled ahead
+constexpr uint32_t kItemReaders = 11;  // 8 softmax warps, MMA, loads, fixer
+constexpr uint32_t kTmemCols = 512;    // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr int kMaxStages = 10;
+
+template <int D>
+struct Lay {
+  static constexpr int kOp = kTileN * D * 2;       // one Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kQOff = 0, kKVOff = 2 * kOp;
+  static constexpr int kBarOff = kKVOff + kStages * kOp;
+  static constexpr int kSmem = kBarOff + 1024 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert(kStages <= kMaxStages, "stage barriers");
+};
+
+struct Item {
+  int start;   // first row of the sequence; < 0: no more items
+  int len;     // its tokens
+  int i0;      // first query of tile A; B follows QT later
+  int h0;      // first q head
+  int nkt[2];  // key tiles of A and B (B: 0 when the sequence ends before it)
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t raw[kMaxStages];  // a V tile whose tail warp 11 has yet to zero
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+  uint64_t done;
+  Item items[kItems];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+__device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
+                                        int32_t* dev_err) {
+  if (mbar_wait(bar, parity)) return *reinterpret_cast<volatile int*>(&B->abort_flag) == 0;
+  flag_error(dev_err, PA_DEVERR_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
+  return false;
+}
+
+// The item stream as one role reads it.
+struct Reader {
+  int k = 0;
+  __device__ __forceinline__ bool next(Bars* B, int32_t* dev_err, Item& it) {
+    const int slot = k % kItems;
+    if (!wait_ok(&B->item_full[slot], (k / kItems) & 1, B, dev_err)) return false;
+    it = B->items[slot];
+    ++k;
+    return it.start >= 0;
+  }
+  // the item is copied: its slot may be filled again (one arrival per reader)
+  __device__ __forceinline__ void done(Bars* B) { mbar_arrive(&B->item_empty[(k - 1) % kItems]); }
+};
+
+// Sequence s: its first row and length (0: nothing to do, or inconsistent).
+__device__ __forceinline__ int seq_span(const PromptParams& p, int s, int& start, bool& bad) {
+  const int a = __ldg(&p.query_start_loc[s]), b = __ldg(&p.query_start_loc[s + 1]);
+  bad = a < 0 || b < a || b > p.total;
+  start = a;
+  return a < 0 || b < a ? 0 : max(0, min(b, p.total) - a);
+}
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tmq,
+                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using L = Lay<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* B = reinterpret_cast<Bars*>(smem + L::kBarOff);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lhb = p.log2_hb, QT = kTileM >> lhb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&B->full[s], 1);
+      mbar_init(&B->empty[s], 1);
+      mbar_init(&B->raw[s], 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(&B->item_full[s], 1);
+      mbar_init(&B->item_empty[s], kItemReaders);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B->q_full[x], 1);
+      mbar_init(&B->q_empty[x], 1);
+      mbar_init(&B->s_full[x], 1);
+      mbar_init(&B->p_half[x], 128);
+      mbar_init(&B->p_full[x], 128);
+      mbar_init(&B->o_full[x], 1);
+      mbar_init(&B->o_free[x], 128);
+    }
+    mbar_init(&B->done, 1);
+    B->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc::alloc(&B->tmem_base, kTmemCols);
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&tmq);
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = B->tmem_base;
+
+  // 384 threads at 168 registers: 64,512 = 256 x 200 + 128 x 96 + 1,024 left
+  if (warp >= kMmaWarp) {
+  tc::regs_dec<96>();
+  if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // per key tile and X = A, B: O_X += P_X V of the tile before, then
+    // S_X = Q_X K^T over the P just read (the tensor core keeps their order)
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
+      constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
+      Reader rd;
+      Item it;
+      bool ok = true, issued = false;
+      uint32_t c = 0;                    // stages used before this item
+      int n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
+      struct {
+        bool on = false, first, last, release;
+        int st;
+        uint32_t par;
+      } pend[2];
+      auto pv = [&](int x) -> bool {
+        auto& w = pend[x];
+        if (w.first && n_items[x] >= 2 &&
+            !wait_ok(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
+          return false;
+        if (!wait_ok(&B->full[w.st], w.par, B, p.dev_err)) return false;
+        const uint32_t bV = sbase + L::kKVOff + w.st * L::kOp;
+        const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
+        const uint32_t par = (n_tiles[x] - 1) & 1;
+#pragma unroll
+        for (int kk = 0; kk < kTileN / 16; ++kk) {  // 16 keys = two 8-row groups of V
+          if (kk == 0 || kk == 4) {
+            if (!wait_ok(kk ? &B->p_full[x] : &B->p_half[x], par, B, p.dev_err)) return false;
+            tc::fence_after();
+          }
+          tc::mma_ts(tO, tP + kk * 8, tc::smem_desc(bV + kk * 2048, 16384), idesc_pv,
+                     (w.first && kk == 0) ? 0u : 1u);
+        }
+        if (w.release) tc::commit(&B->empty[w.st]);
+        if (w.last) tc::commit(&B->o_full[x]);
+        w.on = false;
+        return true;
+      };
+      while (ok && rd.next(B, p.dev_err, it)) {
+        rd.done(B);
+        const int n = max(it.nkt[0], it.nkt[1]);
+        for (int j = 0; j < n && ok; ++j, c += 2) {
+          const int sk = c % NS, sv = (c + 1) % NS;
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (pend[x].on && !(ok = pv(x))) break;
+            if (j >= it.nkt[x]) continue;
+            if (j == 0) {
+              ok = wait_ok(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
+              ++n_items[x];
+            }
+            ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t aQ = sbase + L::kQOff + x * L::kOp, bK = sbase + L::kKVOff + sk * L::kOp;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              tc::mma(tmem + x * 128, tc::smem_desc(aQ + off), tc::smem_desc(bK + off), idesc_s,
+                      kk > 0);
+            }
+            issued = true;
+            ++n_tiles[x];
+            tc::commit(&B->s_full[x]);
+            // the tile's last reader of the two frees its stages
+            const bool lastx = x == 1 || j >= it.nkt[1];
+            if (lastx) tc::commit(&B->empty[sk]);
+            if (j == it.nkt[x] - 1) tc::commit(&B->q_empty[x]);
+            auto& w = pend[x];
+            w.on = true;
+            w.first = j == 0;
+            w.last = j == it.nkt[x] - 1;
+            w.release = lastx;
+            w.st = sv;
+            w.par = ((c + 1) / NS) & 1;
+          }
+        }
       }
-      if (t < a || t >= b) continue;
-      const int hk = h / p.group;
-      const T* k = static_cast<const T*>(p.k) + a * p.k_stride + hk * D;
-      const T* v = static_cast<const T*>(p.v) + a * p.v_stride + hk * D;
-      attend_row<D>(static_cast<T*>(p.out) + i * D,
-                    static_cast<const T*>(p.q) + t * p.q_stride + h * D, k, v,
-                    p.v_stride - p.k_stride, t - a + 1, p.scale_log2, 1.f, sq[warp],
-                    [&](int key) { return key * p.k_stride; }, [](int) { return true; });
+      for (int x = 0; x < 2 && ok; ++x)
+        if (pend[x].on) ok = pv(x);
+      // everything issued above has completed before TMEM is released
+      if (issued) {
+        tc::commit(&B->done);
+        mbar_wait(&B->done, 0);
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      Reader rd;
+      Item it;
+      bool ok = true;
+      uint32_t c = 0;
+      int nq[2] = {0, 0};
+      auto tile = [&](const CUtensorMap* map, int kvh, int row, bool tail) {
+        const int st = c % NS;
+        if (c >= (uint32_t)NS && !wait_ok(&B->empty[st], ((c / NS) - 1) & 1, B, p.dev_err))
+          return false;
+        uint8_t* d = smem + L::kKVOff + st * L::kOp;
+        // the arrival of a V tile with a tail to zero is warp 11's
+        uint64_t* bar = tail ? &B->raw[st] : &B->full[st];
+        mbar_arrive_expect_tx(bar, L::kOp);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tc::tma_load_3d(d + h * 16384, map, bar, 64 * h, kvh, row);
+        ++c;
+        return true;
+      };
+      while (ok && rd.next(B, p.dev_err, it)) {
+        rd.done(B);
+        const int n = max(it.nkt[0], it.nkt[1]), kvh = it.h0 / p.group;
+        for (int j = 0; j < n && ok; ++j) {
+          ok = tile(&tmk, kvh, it.start + j * kTileN, false);
+          for (int x = 0; x < 2 && ok && j == 0; ++x) {
+            if (it.nkt[x] == 0) continue;
+            if (nq[x] > 0) ok = wait_ok(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
+            if (!ok) break;
+            ++nq[x];
+            uint8_t* d = smem + L::kQOff + x * L::kOp;
+            mbar_arrive_expect_tx(&B->q_full[x], L::kOp);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(d + h * 16384, &tmq, &B->q_full[x], 64 * h, it.h0,
+                              it.start + it.i0 + x * QT);
+          }
+          ok = ok && tile(&tmv, kvh, it.start + j * kTileN, (j + 1) * kTileN > it.len);
+        }
+      }
+      // loads in flight land before the CTA exits
+      for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
+        mbar_wait(&B->full[u % NS], (u / NS) & 1);
+      for (int x = 0; x < 2; ++x)
+        if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
+    }
+  } else if (warp == kSchedWarp) {
+    // ------------------------------------------------------------ scheduler
+    // level = position of an item in its sequence, in items; the levels are
+    // walked downwards, within a level the sequences that reach it in order,
+    // and the head groups of each
+    const int hgroups = p.n_q >> lhb, span = 2 * QT;
+    auto items_of = [&](int s) -> int {
+      int start;
+      bool bad;
+      return s < p.num_seqs ? (seq_span(p, s, start, bad) + span - 1) / span : 0;
+    };
+    int top = 0;
+    for (int s = lane; s < p.num_seqs; s += 32) {
+      int start;
+      bool bad;
+      top = max(top, (seq_span(p, s, start, bad) + span - 1) / span);
+      if (bad && blockIdx.x == 0) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
+    }
+    for (int m = 16; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const int first = items_of(lane);  // of the first 32 sequences, kept
+    int level = top, cnt = 0;
+    long long base = 0;  // (sequence, level) pairs before this level
+    bool more = true;
+    for (int k = 0; more; ++k) {
+      // there and back: the CTA that got the longest item of one round gets
+      // the shortest of the next
+      const long long idx = (long long)k * gridDim.x +
+                            ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const long long want = idx / hgroups;
+      while (more && want >= base + cnt) {
+        base += cnt;
+        --level;
+        cnt = 0;
+        if (level < 0) {
+          more = false;
+        } else {
+          int n = first > level;
+          for (int s = 32 + lane; s < p.num_seqs; s += 32) n += items_of(s) > level;
+          cnt = __reduce_add_sync(0xffffffffu, n);
+        }
+      }
+      Item it;
+      it.start = -1;
+      if (more) {
+        int r = (int)(want - base), seq = -1;
+        for (int s0 = 0; seq < 0 && s0 < p.num_seqs; s0 += 32) {
+          const bool has = (s0 == 0 ? first : items_of(s0 + lane)) > level;
+          const uint32_t m = __ballot_sync(0xffffffffu, has);
+          const uint32_t hit = __ballot_sync(
+              0xffffffffu, has && __popc(m & ((1u << lane) - 1u)) == r);
+          if (hit) seq = s0 + __ffs(hit) - 1;
+          r -= __popc(m);
+        }
+        bool bad;
+        it.len = seq_span(p, max(seq, 0), it.start, bad);
+        it.i0 = level * span;
+        it.h0 = (int)(idx % hgroups) << lhb;
+        for (int x = 0; x < 2; ++x) {
+          const int i = it.i0 + x * QT;
+          it.nkt[x] = i < it.len ? (min(it.len, i + QT) + kTileN - 1) / kTileN : 0;
+        }
+      }
+      const int slot = k % kItems;
+      bool ok = k < kItems || wait_ok(&B->item_empty[slot], (k / kItems - 1) & 1, B, p.dev_err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        B->items[slot] = it;
+        mbar_arrive(&B->item_full[slot]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------- rows behind a sequence
+    Reader rd;
+    Item it;
+    uint32_t c = 0, phase = 0;  // stages used; per stage, the parity of its next tail
+    while (__all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+      __syncwarp();
+      if (lane == 0) rd.done(B);
+      const int n = max(it.nkt[0], it.nkt[1]);
+      c += 2 * n;
+      const int valid = it.len - (n - 1) * kTileN;  // rows of the last tile
+      if (valid >= kTileN) continue;
+      const int st = (c - 1) % NS;
+      if (!__all_sync(0xffffffffu, wait_ok(&B->raw[st], (phase >> st) & 1, B, p.dev_err))) break;
+      phase ^= 1u << st;
+      uint8_t* d = smem + L::kKVOff + st * L::kOp;
+      // 128-byte rows; the swizzle stays within a row
+      for (int u = valid * 8 + lane; u < kTileN * 8; u += 32)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<uint4*>(d + h * 16384 + u * 16) = make_uint4(0, 0, 0, 0);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->full[st]);
     }
   }
+  } else {
+    // ------------------------------------------------------------ softmax
+    tc::regs_inc<200>();
+    const int x = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row = TMEM lane
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lanes, tO = tmem + 256 + x * 128 + lanes;
+    const float sl = p.scale_log2;
+    Reader rd;
+    Item it;
+    int t = 0, n_mine = 0;
+    bool ok = true;
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+      __syncwarp();
+      if (lane == 0) rd.done(B);
+      const int nkt = it.nkt[x];
+      if (nkt == 0) continue;
+      const int qw = it.i0 + x * QT + ((q4 * 32) >> lhb);  // the warp's first query
+      const int qi = it.i0 + x * QT + (r >> lhb);          // this row's
+      const bool live = qw < it.len;
+      attn::RowState st{-INFINITY, 0.f};
+      for (int j = 0; j < nkt; ++j, ++t) {
+        ok = __all_sync(0xffffffffu, wait_ok(&B->s_full[x], t & 1, B, p.dev_err));
+        if (!ok) break;
+        if (live) {  // rows behind the sequence: nothing reads their P or O
+          tc::fence_after();
+          const bool full = j * kTileN + kTileN - 1 <= qw && sl > 0.f;
+          uint32_t vis[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = attn::bits_upto(j * kTileN + 32 * w, qi);
+          float s[kTileN];
+          attn::load_scores(tS, s);
+          const float mx = attn::tile_max(s, full, vis, sl);
+          const float mn = fmaxf(st.m, mx);
+          const bool grow = mn > st.m + attn::kRescaleLog2;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = exp2f(st.m - mn);  // 0 on the first tile
+            st.l *= alpha;
+            st.m = mn;
+          }
+          // S of this tile is done, so O += P V of the one before is too
+          if (j > 0 && __any_sync(0xffffffffu, grow)) attn::rescale_o(tO, D, alpha);
+          const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
+          uint32_t pk[32];
+          st.l += attn::tile_weights<BF16, 2>(s, 0, full, sl, neg_m, pk);
+          tc::st32x32b_x32(tS, pk);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&B->p_half[x]);
+          st.l += attn::tile_weights<BF16, 2>(s, 1, full, sl, neg_m, pk);
+          tc::st32x32b_x32(tS + 32, pk);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&B->p_full[x]);
+        } else {
+          mbar_arrive(&B->p_half[x]);
+          mbar_arrive(&B->p_full[x]);
+        }
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, wait_ok(&B->o_full[x], n_mine & 1, B, p.dev_err));
+      if (!ok) break;
+      ++n_mine;
+      const bool valid = qi < it.len;
+      const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+      T16* out = static_cast<T16*>(p.out) +
+                 ((size_t)(it.start + (valid ? qi : 0)) * p.n_q + it.h0 + (r & ((1 << lhb) - 1))) * D;
+      tc::fence_after();
+      if (live) {
+#pragma unroll
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          tc::ld32x32b_x32(tO + cc, o);
+          tc::wait_ld();
+          if (cc + 32 == D) {
+            tc::fence_before();
+            mbar_arrive(&B->o_free[x]);
+          }
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 v;
+              uint32_t* w = &v.x;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<BF16>(__uint_as_float(o[e + 2 * k]) * inv,
+                                   __uint_as_float(o[e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + cc + e) = v;
+            }
+          }
+        }
+      } else {
+        mbar_arrive(&B->o_free[x]);
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool BF16, int D>
+cudaError_t launch_t(const PromptParams& p, const CUtensorMap* tmq, const CUtensorMap* tmk,
+                     const CUtensorMap* tmv, cudaStream_t st) {
+  const cudaError_t attr = cudaFuncSetAttribute(
+      prompt_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
+  if (attr != cudaSuccess) return attr;
+  // no more CTAs than there can be items
+  const int span = 2 * (kTileM >> p.log2_hb);
+  const long long most = ((long long)p.total / span + p.num_seqs) * (p.n_q >> p.log2_hb);
+  const int sms = device_sms();
+  prompt_kernel<BF16, D><<<(unsigned)(most < sms ? most : sms), kThreads, Lay<D>::kSmem, st>>>(
+      p, *tmq, *tmk, *tmv);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptParams& p, int D, bool bf16, cudaStream_t st) {
+cudaError_t launch_prompt(const PromptParams& p, int D, bool bf16, const CUtensorMap* tmq,
+                          const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t st) {
   if (p.total == 0 || p.num_seqs == 0) return cudaSuccess;
-  const long long rows = (long long)p.total * p.n_q;
-  const unsigned grid = (unsigned)((rows + 3) / 4 < 148 * 64 ? (rows + 3) / 4 : 148 * 64);
-  if (bf16)
-    D == 128 ? prompt_rows_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p)
-             : prompt_rows_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
-  else
-    D == 128 ? prompt_rows_kernel<__half, 128><<<grid, 128, 0, st>>>(p)
-             : prompt_rows_kernel<__half, 64><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+  if (D == 128)
+    return bf16 ? launch_t<true, 128>(p, tmq, tmk, tmv, st)
+                : launch_t<false, 128>(p, tmq, tmk, tmv, st);
+  return bf16 ? launch_t<true, 64>(p, tmq, tmk, tmv, st)
+              : launch_t<false, 64>(p, tmq, tmk, tmv, st);
 }
 
 }  // namespace pa

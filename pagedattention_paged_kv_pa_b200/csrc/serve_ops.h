@@ -12,18 +12,24 @@
 
 namespace pa {
 
+// SMs of the current device.
+int device_sms();
+
 // Whole-prompt attention: sequence s owns rows query_start_loc[s] ..
 // query_start_loc[s + 1] - 1 of q, k, v and out.
 struct PromptParams {
   void* out;  // [total][n_q][D]
-  const void *q, *k, *v;
   const int32_t* query_start_loc;
   int32_t* dev_err;
   float scale_log2;  // scale x log2(e)
   int n_q, n_kv, group, num_seqs, total;
-  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int log2_hb;       // heads of a tile: the power of two in the group size, <= 16
 };
-cudaError_t launch_prompt(const PromptParams& p, int D, bool bf16, cudaStream_t st);
+// tmq: 3-D map over q viewed as [total][n_q][D], box {64, 2^log2_hb, 128 /
+// 2^log2_hb}; tmk / tmv: over k and v viewed as [total][n_kv][D], box {64, 1,
+// 128}; all with the 128-byte swizzle.
+cudaError_t launch_prompt(const PromptParams& p, int D, bool bf16, const CUtensorMap* tmq,
+                          const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t st);
 
 // Attention of a tree of drafted tokens over the paged cache.
 struct TreeParams {
