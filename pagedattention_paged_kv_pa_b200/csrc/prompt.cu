@@ -161,89 +161,103 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     // per key tile and X = A, B: O_X += P_X V of the tile before, then
-    // S_X = Q_X K^T over the P just read (the tensor core keeps their order)
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
-      constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
-      Reader rd;
-      Item it;
-      bool ok = true, issued = false;
-      uint32_t c = 0;                    // stages used before this item
-      int n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
-      struct {
-        bool on = false, first, last, release;
-        int st;
-        uint32_t par;
-      } pend[2];
-      auto pv = [&](int x) -> bool {
-        auto& w = pend[x];
-        if (w.first && n_items[x] >= 2 &&
-            !wait_ok(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
-          return false;
-        if (!wait_ok(&B->full[w.st], w.par, B, p.dev_err)) return false;
-        const uint32_t bV = sbase + L::kKVOff + w.st * L::kOp;
-        const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
-        const uint32_t par = (n_tiles[x] - 1) & 1;
+    // S_X = Q_X K^T over the P just read (the tensor core keeps their order).
+    // The whole warp walks the tiles and waits; one lane issues.
+    constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
+    constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
+    const uint64_t dQ = tc::smem_desc(sbase + L::kQOff), dK = tc::smem_desc(sbase + L::kKVOff),
+                   dV = tc::smem_desc(sbase + L::kKVOff, 16384);
+    constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
+    Reader rd;
+    Item it;
+    bool ok = true, issued = false;
+    uint32_t c = 0;  // stages used before this tile
+    int n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
+    struct {
+      bool on = false, first, last, release;
+      int st;
+      uint32_t par;
+    } pend[2];
+    auto pv = [&](int x) -> bool {
+      auto& w = pend[x];
+      if (w.first && n_items[x] >= 2 && !wait_ok(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
+        return false;
+      if (!wait_ok(&B->full[w.st], w.par, B, p.dev_err)) return false;
+      const uint64_t v = dV + w.st * kOpStep;
+      const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
+      const uint32_t par = (n_tiles[x] - 1) & 1;
+      // 16 keys a step = two 8-row groups of V
+      if (!wait_ok(&B->p_half[x], par, B, p.dev_err)) return false;
+      tc::fence_after();
+      if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kTileN / 16; ++kk) {  // 16 keys = two 8-row groups of V
-          if (kk == 0 || kk == 4) {
-            if (!wait_ok(kk ? &B->p_full[x] : &B->p_half[x], par, B, p.dev_err)) return false;
-            tc::fence_after();
-          }
-          tc::mma_ts(tO, tP + kk * 8, tc::smem_desc(bV + kk * 2048, 16384), idesc_pv,
-                     (w.first && kk == 0) ? 0u : 1u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (w.first && kk == 0) ? 0u : 1u);
+      }
+      __syncwarp();
+      if (!wait_ok(&B->p_full[x], par, B, p.dev_err)) return false;
+      tc::fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk) tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
         if (w.release) tc::commit(&B->empty[w.st]);
         if (w.last) tc::commit(&B->o_full[x]);
-        w.on = false;
-        return true;
-      };
-      while (ok && rd.next(B, p.dev_err, it)) {
-        rd.done(B);
-        const int n = max(it.nkt[0], it.nkt[1]);
-        for (int j = 0; j < n && ok; ++j, c += 2) {
-          const int sk = c % NS, sv = (c + 1) % NS;
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (pend[x].on && !(ok = pv(x))) break;
-            if (j >= it.nkt[x]) continue;
-            if (j == 0) {
-              ok = wait_ok(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
-              ++n_items[x];
-            }
-            ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
-            const uint32_t aQ = sbase + L::kQOff + x * L::kOp, bK = sbase + L::kKVOff + sk * L::kOp;
+      }
+      __syncwarp();
+      w.on = false;
+      return true;
+    };
+    while (ok && rd.next(B, p.dev_err, it)) {
+      __syncwarp();
+      if (lane == 0) rd.done(B);
+      __syncwarp();
+      const int n = max(it.nkt[0], it.nkt[1]);
+      for (int j = 0; j < n && ok; ++j, c += 2) {
+        const int sk = c % NS, sv = (c + 1) % NS;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (ok && pend[x].on) ok = pv(x);
+          if (!ok || j >= it.nkt[x]) continue;
+          if (j == 0) {
+            ok = wait_ok(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
+            ++n_items[x];
+          }
+          ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+          if (!ok) continue;
+          tc::fence_after();
+          const bool lastx = x == 1 || j >= it.nkt[1];  // the K tile's last reader of the two
+          const bool last = j == it.nkt[x] - 1;
+          if (tc::elect_one()) {
+            const uint64_t q = dQ + x * kOpStep, k = dK + sk * kOpStep;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-              tc::mma(tmem + x * 128, tc::smem_desc(aQ + off), tc::smem_desc(bK + off), idesc_s,
-                      kk > 0);
+              const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+              tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
             }
-            issued = true;
-            ++n_tiles[x];
             tc::commit(&B->s_full[x]);
-            // the tile's last reader of the two frees its stages
-            const bool lastx = x == 1 || j >= it.nkt[1];
             if (lastx) tc::commit(&B->empty[sk]);
-            if (j == it.nkt[x] - 1) tc::commit(&B->q_empty[x]);
-            auto& w = pend[x];
-            w.on = true;
-            w.first = j == 0;
-            w.last = j == it.nkt[x] - 1;
-            w.release = lastx;
-            w.st = sv;
-            w.par = ((c + 1) / NS) & 1;
+            if (last) tc::commit(&B->q_empty[x]);
           }
+          __syncwarp();
+          issued = true;
+          ++n_tiles[x];
+          pend[x].on = true;
+          pend[x].first = j == 0;
+          pend[x].last = last;
+          pend[x].release = lastx;
+          pend[x].st = sv;
+          pend[x].par = ((c + 1) / NS) & 1;
         }
       }
-      for (int x = 0; x < 2 && ok; ++x)
-        if (pend[x].on) ok = pv(x);
-      // everything issued above has completed before TMEM is released
-      if (issued) {
-        tc::commit(&B->done);
-        mbar_wait(&B->done, 0);
-      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (ok && pend[x].on) ok = pv(x);
+    // everything issued above has completed before TMEM is released
+    if (issued) {
+      if (tc::elect_one()) tc::commit(&B->done);
+      __syncwarp();
+      mbar_wait(&B->done, 0);
     }
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
@@ -435,12 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0 && __any_sync(0xffffffffu, grow)) attn::rescale_o(tO, D, alpha);
           const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
           uint32_t pk[32];
-          st.l += attn::tile_weights<BF16, 2>(s, 0, full, sl, neg_m, pk);
+          st.l += attn::tile_weights<BF16, 0>(s, 0, full, sl, neg_m, pk);
           tc::st32x32b_x32(tS, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
-          st.l += attn::tile_weights<BF16, 2>(s, 1, full, sl, neg_m, pk);
+          st.l += attn::tile_weights<BF16, 0>(s, 1, full, sl, neg_m, pk);
           tc::st32x32b_x32(tS + 32, pk);
           tc::wait_st();
           tc::fence_before();

@@ -156,6 +156,19 @@ __device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t r0, uint32_t r1,
                : "memory");
 }
 
+// true in one lane of the (converged) warp, the same one every time.  An MMA
+// batch issued under this predicate keeps its descriptors in uniform registers;
+// under a divergent branch such as lane == 0 every operand is moved there one
+// by one (measured on whole-prompt attention: ~1,700 clocks to issue the 16
+// MMAs of a tile, more than they take to run).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // 2^x with the hardware approximation (results below 2^-126 flush to zero)
 __device__ __forceinline__ float ex2(float x) {
   float y;
