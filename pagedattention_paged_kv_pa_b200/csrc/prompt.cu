@@ -79,6 +79,7 @@ static_assert(sizeof(Bars) <= 1024, "barriers");
 
 __device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
                                         int32_t* dev_err) {
+  if (mbar_try_wait(bar, parity)) return true;
   if (mbar_wait(bar, parity)) return *reinterpret_cast<volatile int*>(&B->abort_flag) == 0;
   flag_error(dev_err, PA_DEVERR_TIMEOUT);
   *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
@@ -176,13 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     struct {
       bool on = false, first, last, release;
       int st;
-      uint32_t par;
     } pend[2];
+    int vst = 0, q_items[2] = {0, 0};  // stage and parity of the tiles' V
+    uint32_t vpar = 0;
     auto pv = [&](int x) -> bool {
       auto& w = pend[x];
       if (w.first && n_items[x] >= 2 && !wait_ok(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
         return false;
-      if (!wait_ok(&B->full[w.st], w.par, B, p.dev_err)) return false;
       const uint64_t v = dV + w.st * kOpStep;
       const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
       const uint32_t par = (n_tiles[x] - 1) & 1;
@@ -214,16 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = max(it.nkt[0], it.nkt[1]);
       for (int j = 0; j < n && ok; ++j, c += 2) {
         const int sk = c % NS, sv = (c + 1) % NS;
+        // what the next MMAs read besides P has usually landed long before P
+        // is written: waited for first, off the chain P -> O += P V -> S
+        if (pend[0].on || pend[1].on) ok = wait_ok(&B->full[vst], vpar, B, p.dev_err);
+        ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+        vst = sv;
+        vpar = ((c + 1) / NS) & 1;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          if (ok && j == 0 && j < it.nkt[x])
+            ok = wait_ok(&B->q_full[x], q_items[x]++ & 1, B, p.dev_err);
           if (ok && pend[x].on) ok = pv(x);
           if (!ok || j >= it.nkt[x]) continue;
-          if (j == 0) {
-            ok = wait_ok(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
-            ++n_items[x];
-          }
-          ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
-          if (!ok) continue;
+          n_items[x] += j == 0;
           tc::fence_after();
           const bool lastx = x == 1 || j >= it.nkt[1];  // the K tile's last reader of the two
           const bool last = j == it.nkt[x] - 1;
@@ -246,10 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           pend[x].last = last;
           pend[x].release = lastx;
           pend[x].st = sv;
-          pend[x].par = ((c + 1) / NS) & 1;
         }
       }
     }
+    if (pend[0].on || pend[1].on) ok = ok && wait_ok(&B->full[vst], vpar, B, p.dev_err);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       if (ok && pend[x].on) ok = pv(x);
@@ -286,10 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = max(it.nkt[0], it.nkt[1]), kvh = it.h0 / p.group;
         for (int j = 0; j < n && ok; ++j) {
           ok = tile(&tmk, kvh, it.start + j * kTileN, false);
-          for (int x = 0; x < 2 && ok && j == 0; ++x) {
-            if (it.nkt[x] == 0) continue;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j > 0 || it.nkt[x] == 0) continue;
             if (nq[x] > 0) ok = wait_ok(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
-            if (!ok) break;
+            if (!ok) continue;
             ++nq[x];
             uint8_t* d = smem + L::kQOff + x * L::kOp;
             mbar_arrive_expect_tx(&B->q_full[x], L::kOp);
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
         mbar_wait(&B->full[u % NS], (u / NS) & 1);
+#pragma unroll
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
     }
@@ -364,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.len = seq_span(p, max(seq, 0), it.start, bad);
         it.i0 = level * span;
         it.h0 = (int)(idx % hgroups) << lhb;
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int i = it.i0 + x * QT;
           it.nkt[x] = i < it.len ? (min(it.len, i + QT) + kTileN - 1) / kTileN : 0;
@@ -419,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
       __syncwarp();
       if (lane == 0) rd.done(B);
-      const int nkt = it.nkt[x];
+      const int nkt = x ? it.nkt[1] : it.nkt[0];
       if (nkt == 0) continue;
       const int qw = it.i0 + x * QT + ((q4 * 32) >> lhb);  // the warp's first query
       const int qi = it.i0 + x * QT + (r >> lhb);          // this row's
