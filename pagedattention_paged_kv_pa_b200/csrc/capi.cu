@@ -485,8 +485,10 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
 
 size_t pa_decode_tree_workspace_size(int num_seqs, int q_len, int n_q_heads, int n_kv_heads,
                                      int head_dim) {
-  (void)num_seqs, (void)q_len, (void)n_q_heads, (void)n_kv_heads, (void)head_dim;
-  return 0;
+  if (num_seqs < 1 || q_len < 1 || q_len > 64 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
+      n_q_heads / n_kv_heads > 8 || head_dim < 1)
+    return 0;
+  return pa::tree_ws_bytes(q_len, n_q_heads / n_kv_heads, head_dim);
 }
 
 pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -526,7 +528,7 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
   p.masks = masks;
   p.dev_err = dev_err;
   p.scale_log2 = scale * kLog2e * (fp8 ? k_scale : 1.f);
-  p.out_mul = fp8 ? v_scale : 1.f;
+  p.out_mul = fp8 ? v_scale * kFp8VUnscale : 1.f;
   p.n_q = n_q_heads;
   p.n_kv = n_kv_heads;
   p.group = n_q_heads / n_kv_heads;
@@ -534,8 +536,15 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
   p.q_len = q_len;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
-  return cuda_status(pa::launch_tree(p, head_dim, q_dtype == PA_BF16, fp8,
-                                     static_cast<cudaStream_t>(stream)));
+  p.q_box_nodes = std::min(q_len, 128 / p.group);
+  CUtensorMap tmq, tmk, tmv;
+  if (!kv_pool_map(k_pool, num_blocks, n_kv_heads, head_dim, kv_dtype, &tmk) ||
+      !kv_pool_map(v_pool, num_blocks, n_kv_heads, head_dim, kv_dtype, &tmv) ||
+      !tokens_map(q, num_seqs * q_len, n_q_heads, head_dim, (int64_t)n_q_heads * head_dim, p.group,
+                  p.q_box_nodes, &tmq))
+    return PA_ERR_CUDA;
+  return cuda_status(pa::launch_tree(p, head_dim, q_dtype == PA_BF16, fp8, workspace, &tmq, &tmk,
+                                     &tmv, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_tree_masks(const int32_t* parents, const int32_t* tree_lens, int num_seqs,
@@ -740,7 +749,7 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
     // operands widen exactly there, so V needs no 2^-8 fold
     const uint64_t rows = (uint64_t)n_chunks * n_kv_heads * p.stage_rows;
     if (rows >= (uint64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
-    p.out_mul = fp8 ? v_scale : 1.f;
+    p.out_mul = fp8 ? v_scale * kFp8VUnscale : 1.f;
     const uint16_t* kst = static_cast<const uint16_t*>(workspace);
     if (!get_map(kst, rows, 128, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &tmk) ||
         !get_map(kst + rows * 128, rows, 128, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &tmv))

@@ -86,6 +86,12 @@ __device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
   return false;
 }
 
+// the same for a whole warp, which goes on or gives up together
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
+                                         int32_t* dev_err) {
+  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
+}
+
 // The item stream as one role reads it.
 struct Reader {
   int k = 0;
@@ -182,13 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t vpar = 0;
     auto pv = [&](int x) -> bool {
       auto& w = pend[x];
-      if (w.first && n_items[x] >= 2 && !wait_ok(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
+      if (w.first && n_items[x] >= 2 && !wait_all(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
         return false;
       const uint64_t v = dV + w.st * kOpStep;
       const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
       const uint32_t par = (n_tiles[x] - 1) & 1;
       // 16 keys a step = two 8-row groups of V
-      if (!wait_ok(&B->p_half[x], par, B, p.dev_err)) return false;
+      if (!wait_all(&B->p_half[x], par, B, p.dev_err)) return false;
       tc::fence_after();
       if (tc::elect_one()) {
 #pragma unroll
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (w.first && kk == 0) ? 0u : 1u);
       }
       __syncwarp();
-      if (!wait_ok(&B->p_full[x], par, B, p.dev_err)) return false;
+      if (!wait_all(&B->p_full[x], par, B, p.dev_err)) return false;
       tc::fence_after();
       if (tc::elect_one()) {
 #pragma unroll
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.on = false;
       return true;
     };
-    while (ok && rd.next(B, p.dev_err, it)) {
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
       __syncwarp();
       if (lane == 0) rd.done(B);
       __syncwarp();
@@ -217,14 +223,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sk = c % NS, sv = (c + 1) % NS;
         // what the next MMAs read besides P has usually landed long before P
         // is written: waited for first, off the chain P -> O += P V -> S
-        if (pend[0].on || pend[1].on) ok = wait_ok(&B->full[vst], vpar, B, p.dev_err);
-        ok = ok && wait_ok(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+        if (pend[0].on || pend[1].on) ok = wait_all(&B->full[vst], vpar, B, p.dev_err);
+        ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
         vst = sv;
         vpar = ((c + 1) / NS) & 1;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (ok && j == 0 && j < it.nkt[x])
-            ok = wait_ok(&B->q_full[x], q_items[x]++ & 1, B, p.dev_err);
+            ok = wait_all(&B->q_full[x], q_items[x]++ & 1, B, p.dev_err);
           if (ok && pend[x].on) ok = pv(x);
           if (!ok || j >= it.nkt[x]) continue;
           n_items[x] += j == 0;
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (pend[0].on || pend[1].on) ok = ok && wait_ok(&B->full[vst], vpar, B, p.dev_err);
+    if (pend[0].on || pend[1].on) ok = ok && wait_all(&B->full[vst], vpar, B, p.dev_err);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       if (ok && pend[x].on) ok = pv(x);

@@ -41,8 +41,22 @@ struct TreeParams {
   float scale_log2;  // scale x log2(e) (x k_scale for fp8 caches)
   float out_mul;     // v_scale for fp8 caches, else 1
   int n_q, n_kv, group, num_seqs, q_len, max_blocks, num_blocks;
+  int q_box_nodes;  // nodes of the query map's box
+  // set by launch_tree
+  float* ws_o;     // [CTA][2 slots][rows][D] unnormalised segment outputs
+  float2* ws_ml;   // [CTA][2 slots][rows] (log2-domain maximum, sum)
+  int row_groups;  // CTAs side by side over the same keys
+  int step_keys;   // keys of a step of the work split
 };
-cudaError_t launch_tree(const TreeParams& p, int D, bool bf16, bool fp8, cudaStream_t st);
+constexpr int kTreeCtas = 148;  // most CTAs of a launch: the workspace is laid out for them
+size_t tree_ws_bytes(int q_len, int group, int D);
+// tmq (16-bit caches): 3-D map over q viewed as [num_seqs x q_len][n_q][D], box
+// {64, group, q_box_nodes}, q_box_nodes = min(q_len, 128 / group); tmk / tmv:
+// 2-D maps over the pools viewed as [num_blocks x n_kv x 16][D], box {64, 16}
+// with the 128-byte swizzle, for E4M3 {D, 16} with the D-byte swizzle.
+cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspace,
+                        const CUtensorMap* tmq, const CUtensorMap* tmk, const CUtensorMap* tmv,
+                        cudaStream_t st);
 
 // Moving the accepted tokens' rows, all layers of a launch at once.
 constexpr int kCompactLayers = 64;  // layers per launch (pointers travel as arguments)

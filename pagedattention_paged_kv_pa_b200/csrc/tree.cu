@@ -1,61 +1,940 @@
-// Attention of a tree of drafted tokens over the paged cache
-// (pa_decode_tree): one warp per (sequence, node, head).
-#include "attn_rows.cuh"
+// Attention of a tree of drafted tokens over the paged cache (pa_decode_tree)
+// on tcgen05 tensor cores.
+//
+// Node i of a sequence attends to the prefix and to the nodes of its mask:
+// out = sum of 2^(s_u - m) v_u / l over those keys u, s = scale log2(e) q . k,
+// in one pass with the running (m, l) of attn_tile.cuh.  Only the last tiles
+// of a context hold tree nodes; there a row's 64-bit mask, shifted to the
+// tile, says which keys it sees.
+//
+// Rows.  For one (sequence, kv head) the (node, query head) pairs are rows of
+// 128-row tiles, QT = floor(128 / G) nodes of G heads to a tile, so that a K/V
+// tile of 128 keys is read once for all heads of its kv head.  A CTA holds two
+// tiles, A and B, in TMEM (S 128 fp32 columns, P over S as 16-bit pairs, O):
+// the tensor cores work on one while the softmax of the other runs.
+//  - Trees of one tile (SPLIT): A and B are the same rows over alternate key
+//    tiles, merged at the end of a run of keys.  K/V bytes bound these.
+//  - Larger trees: A and B are two row tiles over the same keys; trees of more
+//    than two tiles take two CTAs side by side over the same keys (the second
+//    reader of a K/V tile finds it in L2).
+//
+// Work split.  Persistent CTAs.  The (sequence, kv head) units lie end to end,
+// measured in key steps (256 keys when split, else 128) plus kSegCost steps'
+// worth of time for a unit's fixed costs; share c of C is [c T / C, (c + 1) T /
+// C) of the total T.  A run of a unit's steps inside one share is a segment.  A
+// segment that is the whole unit writes the output; others write their
+// unnormalised O and (m, l) to one of their CTA's two workspace slots (0: the
+// unit began in an earlier share, 1: it ends in a later one), which
+// tree_merge_kernel, a programmatic dependent, combines in share order.
+//
+// Roles: warps 0-3 softmax of A, 4-7 of B (one thread per row), warp 8 owns
+// TMEM and issues the MMAs, warp 9 loads Q and K, warp 10 V (16-token blocks
+// by TMA through the block table; rows of the block a context ends in are
+// copied, rows past it and blocks with a bad id zeroed by the warp itself),
+// warp 11 walks the share.  E4M3 caches: warp 9 brings the raw K and V rows
+// into a ring of raw tiles and warps 12-15 widen them to the f16 operands (K
+// exactly, V as code x 2^-8, exactly too, undone by the output scale); the
+// softmax threads write their query rows, scaled by a power of two into f16's
+// range when they are bf16, and P is f16.  Every wait is bounded; a role that
+// gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its loads
+// and MMAs and frees TMEM.
+#include <type_traits>
+
+#include "attn_tile.cuh"
 #include "serve_ops.h"
 
 namespace pa {
 
 namespace {
 
-template <typename T, typename KvT, int D>
-__global__ void __launch_bounds__(128) tree_rows_kernel(const TreeParams p) {
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x >> 5;
-  const long long rows = (long long)p.num_seqs * p.q_len * p.n_q;
-  for (long long i = blockIdx.x * 4ll + warp; i < rows; i += gridDim.x * 4ll) {
-    const int h = (int)(i % p.n_q);
-    const long long sn = i / p.n_q;
-    const int node = (int)(sn % p.q_len), s = (int)(sn / p.q_len);
-    const int raw_c = p.context_lens[s], raw_n = p.tree_lens ? p.tree_lens[s] : p.q_len;
-    const int ctx = min(max(raw_c, 0), p.max_blocks * 16), n = min(max(raw_n, 0), p.q_len);
-    if (raw_c > ctx) flag_error(p.dev_err, PA_DEVERR_BLOCK_ID);
-    if (raw_n != n) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
-    const int32_t* bt = p.block_tables + (size_t)s * p.max_blocks;
-    const uint64_t mask = node < n ? p.masks[sn] : 0;
-    const int P = ctx - n;
-    attend_row<D>(
-        static_cast<T*>(p.out) + i * D, static_cast<const T*>(p.q) + i * D,
-        static_cast<const KvT*>(p.k_pool), static_cast<const KvT*>(p.v_pool), 0ll,
-        node < n ? ctx : 0, p.scale_log2, p.out_mul, sq[warp],
-        [&](int key) -> long long {
-          const int b = bt[key >> 4];
-          if (b < 0 || b >= p.num_blocks) {
-            flag_error(p.dev_err, PA_DEVERR_BLOCK_ID);
-            return -1;
-          }
-          return (((long long)b * p.n_kv + h / p.group) * 16 + (key & 15)) * D;
-        },
-        [&](int key) { return key < P || (mask >> (key - P)) & 1; });
+using attn::kTileM;
+using attn::kTileN;
+
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
+constexpr int kSegs = 4;  // segments scheduled ahead
+constexpr uint32_t kTmemCols = 512;  // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr int kSegCost = 1;  // a unit's fixed costs, in steps
+
+template <int D, bool FP8, bool SPLIT>
+struct Lay {
+  static constexpr int kOp = kTileN * D * 2;  // one 16-bit Q, K or V tile
+  static constexpr int kRaw = kTileN * D;     // one E4M3 K or V tile
+  static constexpr int kQ = SPLIT ? 1 : 2;    // Q tiles
+  static constexpr int kScale = 128 / D;
+  static constexpr int kKS = (FP8 ? 2 : 3) * kScale;
+  static constexpr int kVS = (FP8 && !SPLIT && D == 128 ? 1 : 2) * kScale;
+  static constexpr int kRS = FP8 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQOff + kQ * kOp;
+  static constexpr int kVOff = kKOff + kKS * kOp;
+  static constexpr int kRawOff = kVOff + kVS * kOp;
+  static constexpr int kRedOff = kRawOff + kRS * kRaw;  // [2][2][128] float2
+  static constexpr int kBarOff = kRedOff + (SPLIT ? 4096 : 0);
+  static constexpr int kSmem = kBarOff + 1024 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  // registers: 512 x 128 = 256 x 176 + 256 x 80, or 384 x 168 = 256 x 200 +
+  // 128 x 96 + 1,024
+  static constexpr int kSoftRegs = FP8 ? 176 : 200, kOtherRegs = FP8 ? 80 : 96;
+  // readers of a segment: 8 softmax warps, MMA, loads (K, V), 4 converters
+  static constexpr uint32_t kReaders = FP8 ? 14 : 11;
+};
+
+struct Seg {
+  int s, h;    // s < 0: no more
+  int ctx, n;  // context length, nodes
+  int t0, t1;  // key tiles
+  int slot;    // workspace slot, or -1: the whole unit
+};
+
+struct Bars {
+  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], raw_full[4], raw_empty[4];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], red[2];
+  uint64_t done;
+  Seg segs[kSegs];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+__device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
+                                        int32_t* dev_err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_wait(bar, parity)) return *reinterpret_cast<volatile int*>(&B->abort_flag) == 0;
+  flag_error(dev_err, PA_DEVERR_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
+  return false;
+}
+
+// the same for a whole warp, which goes on or gives up together
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
+                                         int32_t* dev_err) {
+  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
+}
+
+// The segment stream as one role reads it.
+struct Reader {
+  int k = 0;
+  __device__ __forceinline__ bool next(Bars* B, int32_t* dev_err, Seg& g) {
+    const int slot = k % kSegs;
+    if (!wait_ok(&B->seg_full[slot], (k / kSegs) & 1, B, dev_err)) return false;
+    g = B->segs[slot];
+    ++k;
+    return g.s >= 0;
+  }
+  __device__ __forceinline__ void done(Bars* B) { mbar_arrive(&B->seg_empty[(k - 1) % kSegs]); }
+};
+
+// ------------------------------------------------------------- work split
+__device__ __forceinline__ int seq_ctx(const TreeParams& p, int s) {
+  return min(max(__ldg(&p.context_lens[s]), 0), p.max_blocks * 16);
+}
+__device__ __forceinline__ int seq_nodes(const TreeParams& p, int s) {
+  return p.tree_lens ? min(max(__ldg(&p.tree_lens[s]), 0), p.q_len) : p.q_len;
+}
+__device__ __forceinline__ int seq_steps(const TreeParams& p, int s) {
+  const int n = seq_nodes(p, s), c = seq_ctx(p, s);
+  return n > 0 ? (c + p.step_keys - 1) / p.step_keys : 0;
+}
+__device__ __forceinline__ int weight(int steps) { return steps > 0 ? steps + kSegCost : 0; }
+
+// T, by one warp; flags lengths out of range when `report`
+__device__ long long total_weight(const TreeParams& p, int lane, bool report) {
+  long long part = 0;
+  int err = 0;
+  for (int s = lane; s < p.num_seqs; s += 32) {
+    part += weight(seq_steps(p, s));
+    if (report) {
+      const int n = p.tree_lens ? __ldg(&p.tree_lens[s]) : p.q_len;
+      if (n < 0 || n > p.q_len) err |= PA_DEVERR_QUERY_LOC;
+      if (__ldg(&p.context_lens[s]) > p.max_blocks * 16) err |= PA_DEVERR_BLOCK_ID;
+    }
+  }
+  if (err) flag_error(p.dev_err, err);
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) part += __shfl_xor_sync(0xffffffffu, part, m);
+  return part * p.n_kv;
+}
+// floor(c T / C) without overflow
+__device__ __forceinline__ long long share_start(long long T, long long c, long long C) {
+  return (T / C) * c + (T % C) * c / C;
+}
+// The sequence whose span [gs, gs + n_kv w) of positions holds X, by one warp.
+__device__ bool locate(const TreeParams& p, long long X, int lane, int& s_out, long long& gs_out,
+                       int& w_out) {
+  long long acc = 0;
+  for (int base = 0; base < p.num_seqs; base += 32) {
+    const int s = base + lane;
+    const int n = s < p.num_seqs ? weight(seq_steps(p, s)) : 0;
+    int incl = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += v;
+    }
+    const long long gs = acc + (long long)(incl - n) * p.n_kv;
+    const long long ge = acc + (long long)incl * p.n_kv;
+    const uint32_t hit = __ballot_sync(0xffffffffu, gs <= X && X < ge);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s_out = __shfl_sync(0xffffffffu, s, src);
+      gs_out = __shfl_sync(0xffffffffu, gs, src);
+      w_out = __shfl_sync(0xffffffffu, n, src);
+      return true;
+    }
+    acc += (long long)__shfl_sync(0xffffffffu, incl, 31) * p.n_kv;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------- tiles
+// 16-bit operand tile with the 128-byte swizzle: 128 rows of 64 elements in
+// D / 64 halves 16 KiB apart; chunk = 8 consecutive elements
+__device__ __forceinline__ uint32_t op_off(int row, int chunk) {
+  return (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+// E4M3 tile: 128 rows of D bytes, 128- or 64-byte swizzle; chunk = 16 codes
+template <int D>
+__device__ __forceinline__ uint32_t raw_off(int row, int chunk) {
+  return D == 128 ? swz128(row * 128 + chunk * 16) : swz64(row * 64 + chunk * 16);
+}
+
+// Loads tile t of a (sequence, kv head) into `dst`, by one warp: whole blocks
+// of the context by TMA, the other rows written here.
+template <int D, bool FP8>
+__device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int t, uint8_t* dst,
+                                          const CUtensorMap* map, const uint8_t* pool,
+                                          uint64_t* full, int lane, bool report,
+                                          uint64_t policy) {
+  constexpr int kRow = FP8 ? D : 2 * D;  // bytes of a row
+  const int blk = t * 8 + lane;
+  const bool in_ctx = lane < 8 && blk * 16 < g.ctx;
+  const int phys = in_ctx ? __ldg(&p.block_tables[(size_t)g.s * p.max_blocks + blk]) : -1;
+  const bool in_range = phys >= 0 && phys < p.num_blocks;
+  if (report && in_ctx && !in_range) flag_error(p.dev_err, PA_DEVERR_BLOCK_ID);
+  const bool whole = in_ctx && in_range && blk * 16 + 16 <= g.ctx;
+  const uint32_t whole_m = __ballot_sync(0xffffffffu, whole);
+  for (uint32_t pm = __ballot_sync(0xffffffffu, lane < 8 && !whole); pm; pm &= pm - 1) {
+    const int m = __ffs(pm) - 1;
+    const int ph = __shfl_sync(0xffffffffu, phys, m);
+    const bool ok_id = ph >= 0 && ph < p.num_blocks;
+    const int nvalid = ok_id ? max(0, min(16, g.ctx - (t * 8 + m) * 16)) : 0;
+    const uint8_t* src = pool + (long long)(ok_id ? ph * p.n_kv + g.h : 0) * 16 * kRow;
+#pragma unroll
+    for (int u = 0; u < kRow / 32; ++u) {  // 16 rows of kRow / 16 chunks
+      const int idx = lane + 32 * u, r = idx / (kRow / 16), cc = idx % (kRow / 16);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < nvalid) v = __ldg(reinterpret_cast<const uint4*>(src + r * kRow + cc * 16));
+      *reinterpret_cast<uint4*>(dst + (FP8 ? raw_off<D>(16 * m + r, cc)
+                                           : op_off(16 * m + r, cc))) = v;
+    }
+  }
+  tc::fence_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_expect_tx(full, __popc(whole_m) * 16u * kRow);
+  __syncwarp();
+  if (whole) {
+    const int y = (phys * p.n_kv + g.h) * 16;  // row of the [rows][D] view
+    if constexpr (FP8) {
+      tma_load_2d_hint(dst + lane * 16 * kRow, map, full, 0, y, policy);
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_2d_hint(dst + h * 16384 + lane * 2048, map, full, 64 * h, y, policy);
+    }
   }
 }
 
-template <typename T, typename KvT>
-cudaError_t launch_t(const TreeParams& p, int D, cudaStream_t st) {
-  const long long rows = (long long)p.num_seqs * p.q_len * p.n_q;
-  const unsigned grid = (unsigned)((rows + 3) / 4 < 148 * 64 ? (rows + 3) / 4 : 148 * 64);
-  D == 128 ? tree_rows_kernel<T, KvT, 128><<<grid, 128, 0, st>>>(p)
-           : tree_rows_kernel<T, KvT, 64><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+// bits of keys first .. first + 31 that a row with tree mask `mask` and the
+// prefix 0 .. P - 1 sees
+__device__ __forceinline__ uint32_t seen_bits(int first, int P, uint64_t mask) {
+  const int sh = first - P;  // the node at the first key
+  if (sh <= -32) return 0xffffffffu;
+  if (sh < 0) return (uint32_t)(mask << -sh) | ((1u << -sh) - 1u);
+  return sh < 64 ? (uint32_t)(mask >> sh) : 0u;
+}
+
+template <bool BF16, int D, bool FP8, bool SPLIT>
+__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
+    tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmq,
+                const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using L = Lay<D, FP8, SPLIT>;
+  constexpr bool kOpBf16 = BF16 && !FP8;  // the operands' type
+  constexpr int KS = L::kKS, VS = L::kVS, RS = FP8 ? L::kRS : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* B = reinterpret_cast<Bars*>(smem + L::kBarOff);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nrg = p.row_groups, rg = blockIdx.x % nrg;  // CTAs side by side
+  const int G = p.group, QT = kTileM / G;
+  // nodes of this CTA's tile X that sequence g has
+  auto tile_nodes = [&](const Seg& g, int x) -> int {
+    return max(0, min(QT, g.n - (SPLIT ? 0 : 2 * rg + x) * QT));
+  };
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&B->k_full[s], FP8 ? 128 : 1);
+      mbar_init(&B->k_empty[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&B->v_full[s], FP8 ? 128 : 1);
+      mbar_init(&B->v_empty[s], 1);
+    }
+    for (int s = 0; s < RS; ++s) {
+      mbar_init(&B->raw_full[s], 1);
+      mbar_init(&B->raw_empty[s], 128);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&B->seg_full[s], 1);
+      mbar_init(&B->seg_empty[s], L::kReaders);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&B->q_full[x], FP8 ? 128 : 1);
+      mbar_init(&B->q_empty[x], 1);
+      mbar_init(&B->s_full[x], 1);
+      mbar_init(&B->p_half[x], 128);
+      mbar_init(&B->p_full[x], 128);
+      mbar_init(&B->o_full[x], 1);
+      mbar_init(&B->o_free[x], SPLIT ? 256 : 128);
+      mbar_init(&B->red[x], 128);
+    }
+    mbar_init(&B->done, 1);
+    B->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc::alloc(&B->tmem_base, kTmemCols);
+  if (warp == kKWarp && lane == 0) {
+    if (!FP8) prefetch_tensormap(&tmq);
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = B->tmem_base;
+
+  if (warp >= kMmaWarp) {
+    tc::regs_dec<L::kOtherRegs>();
+    if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer
+      // per step and X = A, B: O_X += P_X V of the step before, then
+      // S_X = Q_X K^T over the P just read.  The whole warp walks the steps
+      // and waits; one lane issues.
+      constexpr uint32_t idesc_s = tc::idesc_f16(kOpBf16, false, kTileM, kTileN);
+      constexpr uint32_t idesc_pv = tc::idesc_f16(kOpBf16, true, kTileM, D);
+      constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
+      const uint64_t dQ = tc::smem_desc(sbase + L::kQOff), dK = tc::smem_desc(sbase + L::kKOff),
+                     dV = tc::smem_desc(sbase + L::kVOff, 16384);
+      Reader rd;
+      Seg g;
+      bool ok = true, issued = false;
+      uint32_t c = 0;  // key tiles before this segment
+      int n_segs = 0, n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
+      struct {
+        bool on = false, first, last, release;
+        uint32_t tile;  // its V tile, counted over all segments
+        int before;     // O buffers of X read out before this one (for `first`)
+      } pend[2];
+      auto pv = [&](int x) -> bool {
+        auto& w = pend[x];
+        if (w.first && w.before > 0 &&
+            !wait_all(&B->o_free[x], (w.before - 1) & 1, B, p.dev_err))
+          return false;
+        const int st = w.tile % VS;
+        if (!wait_all(&B->v_full[st], (w.tile / VS) & 1, B, p.dev_err)) return false;
+        const uint64_t v = dV + st * kOpStep;
+        const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
+        const uint32_t par = (n_tiles[x] - 1) & 1;
+        if (!wait_all(&B->p_half[x], par, B, p.dev_err)) return false;
+        tc::fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
+            tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (w.first && kk == 0) ? 0u : 1u);
+        }
+        __syncwarp();
+        if (!wait_all(&B->p_full[x], par, B, p.dev_err)) return false;
+        tc::fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+          if (w.release) tc::commit(&B->v_empty[st]);
+          if (w.last) tc::commit(&B->o_full[x]);
+        }
+        __syncwarp();
+        w.on = false;
+        return true;
+      };
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+        __syncwarp();
+        if (lane == 0) rd.done(B);
+        const int nt = g.t1 - g.t0, steps = SPLIT ? (nt + 1) / 2 : nt;
+        const bool live1 = SPLIT ? nt > 1 : tile_nodes(g, 1) > 0;  // A always has a tile
+        if (SPLIT) {
+          // E4M3: the query rows come from the softmax threads, after the
+          // segment before, whose last products they wait for
+          if (FP8 && pend[0].on) ok = pv(0);
+          if (FP8 && ok && pend[1].on) ok = pv(1);
+          ok = ok && wait_all(&B->q_full[0], n_segs & 1, B, p.dev_err);
+        }
+        for (int j = 0; j < steps && ok; ++j) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ok && pend[x].on) ok = pv(x);
+            const int ti = SPLIT ? 2 * j + x : j;
+            if (!ok || ti >= nt || (x == 1 && !live1)) continue;
+            if (!SPLIT && j == 0) ok = wait_all(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
+            const uint32_t tile = c + ti;
+            const int sk = tile % KS;
+            ok = ok && wait_all(&B->k_full[sk], (tile / KS) & 1, B, p.dev_err);
+            if (!ok) continue;
+            tc::fence_after();
+            const bool lastx = SPLIT || x == 1 || !live1;  // the K/V tile's last reader
+            const bool last = SPLIT ? ti + 2 >= nt : j == nt - 1;
+            if (tc::elect_one()) {
+              const uint64_t q = dQ + (SPLIT ? 0 : x) * kOpStep, k = dK + sk * kOpStep;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+                tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
+              }
+              tc::commit(&B->s_full[x]);
+              if (lastx) tc::commit(&B->k_empty[sk]);
+              if (SPLIT ? ti == nt - 1 : last) tc::commit(&B->q_empty[SPLIT ? 0 : x]);
+            }
+            __syncwarp();
+            issued = true;
+            ++n_tiles[x];
+            pend[x].on = true;
+            pend[x].first = j == 0;
+            pend[x].last = last;
+            pend[x].release = lastx;
+            pend[x].tile = tile;
+            if (j == 0) pend[x].before = SPLIT ? n_segs : n_items[x]++;
+          }
+        }
+        c += nt;
+        ++n_segs;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (ok && pend[x].on) ok = pv(x);
+      // everything issued above has completed before TMEM is released
+      if (issued) {
+        if (tc::elect_one()) tc::commit(&B->done);
+        __syncwarp();
+        mbar_wait(&B->done, 0);
+      }
+    } else if (warp == kKWarp || (!FP8 && warp == kVWarp)) {
+      // ---------------------------------------------------------------- loads
+      // 16-bit caches: K (with Q) and V by a warp each; E4M3: K and V of each
+      // tile in turn through one ring of raw tiles
+      const bool vop = warp == kVWarp;
+      const int NS = FP8 ? RS : (vop ? VS : KS);
+      uint64_t* full = FP8 ? B->raw_full : (vop ? B->v_full : B->k_full);
+      uint64_t* empty = FP8 ? B->raw_empty : (vop ? B->v_empty : B->k_empty);
+      uint8_t* ring = smem + (FP8 ? L::kRawOff : (vop ? L::kVOff : L::kKOff));
+      constexpr int kStage = FP8 ? L::kRaw : L::kOp;
+      const uint64_t policy = l2_policy_evict_first();  // K/V are read once
+      Reader rd;
+      Seg g;
+      bool ok = true;
+      uint32_t c = 0;
+      int nq[2] = {0, 0};
+      auto tile = [&](int t, bool v) -> bool {
+        const int st = c % NS;
+        const bool w = c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+        if (!__all_sync(0xffffffffu, w)) return false;
+        load_tile<D, FP8>(p, g, t, ring + st * kStage, v ? &tmv : &tmk,
+                          static_cast<const uint8_t*>(v ? p.v_pool : p.k_pool), &full[st], lane,
+                          !v, policy);
+        ++c;
+        return true;
+      };
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+        __syncwarp();
+        if (lane == 0) rd.done(B);
+        for (int t = g.t0; t < g.t1 && ok; ++t) {
+          ok = tile(t, vop);
+          if (FP8) {
+            ok = ok && tile(t, true);
+          } else if (!vop && t == g.t0) {
+#pragma unroll
+            for (int x = 0; x < L::kQ; ++x) {
+              if (!ok || tile_nodes(g, x) == 0) continue;
+              const bool w =
+                  nq[x] == 0 || wait_ok(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
+              ok = __all_sync(0xffffffffu, w);
+              if (!ok) continue;
+              ++nq[x];
+              if (lane == 0) {
+                uint8_t* d = smem + L::kQOff + x * L::kOp;
+                const int node = (SPLIT ? 0 : 2 * rg + x) * QT;
+                mbar_arrive_expect_tx(&B->q_full[x], p.q_box_nodes * G * D * 2);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  tc::tma_load_3d(d + h * 16384, &tmq, &B->q_full[x], 64 * h, g.h * G,
+                                  g.s * p.q_len + node);
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      // loads in flight land before the CTA exits
+      for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
+        mbar_wait(&full[u % NS], (u / NS) & 1);
+      if (!FP8)
+#pragma unroll
+        for (int x = 0; x < L::kQ; ++x)
+          if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
+    } else if (warp == kSchedWarp) {
+      // ------------------------------------------------------------ scheduler
+      const long long T = total_weight(p, lane, blockIdx.x == 0);
+      const long long C = gridDim.x / nrg, sc = blockIdx.x / nrg;
+      const long long gbeg = share_start(T, sc, C), gend = share_start(T, sc + 1, C);
+      int s = 0, w = 0, h = 0, step = 0;
+      long long gs = 0;
+      bool more = gbeg < gend && locate(p, gbeg, lane, s, gs, w);
+      if (more) {
+        h = (int)((gbeg - gs) / w);
+        step = max(0, (int)((gbeg - gs) % w) - kSegCost);
+      }
+      for (int k = 0;;) {
+        Seg g;
+        g.s = -1;
+        bool emit = !more;
+        if (more) {
+          const int steps = w - kSegCost;
+          const long long u = gs + (long long)h * w + kSegCost;  // of the unit's first step
+          if (u + step >= gend) {
+            more = false;
+            continue;
+          }
+          const int end = (int)min((long long)steps, gend - u);
+          g.s = s;
+          g.h = h;
+          g.ctx = seq_ctx(p, s);
+          g.n = seq_nodes(p, s);
+          const int tps = p.step_keys / kTileN, nt = (g.ctx + kTileN - 1) / kTileN;
+          g.t0 = step * tps;
+          g.t1 = min(nt, end * tps);
+          g.slot = step > 0 ? 0 : (end < steps ? 1 : -1);
+          emit = tile_nodes(g, 0) > 0;  // the second CTA of a small tree has no rows
+          step = 0;
+          if (end < steps) {
+            more = false;
+          } else if (++h == p.n_kv) {
+            h = 0;
+            gs += (long long)p.n_kv * w;
+            do {
+              ++s;
+              w = s < p.num_seqs ? weight(seq_steps(p, s)) : 0;
+            } while (s < p.num_seqs && w == 0);
+            more = s < p.num_seqs;
+          }
+        }
+        if (!emit) continue;
+        const int slot = k % kSegs;
+        const bool ok = k < kSegs || wait_ok(&B->seg_empty[slot], (k / kSegs - 1) & 1, B, p.dev_err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          B->segs[slot] = g;
+          mbar_arrive(&B->seg_full[slot]);
+        }
+        __syncwarp();
+        ++k;
+        if (g.s < 0) break;
+      }
+    } else if (FP8 && warp >= 12) {
+      // ----------------------------------------------------------- converters
+      const int ct = threadIdx.x - 384;  // 0 .. 127
+      constexpr int kCh = D / 16;        // 16-code chunks of a row
+      Reader rd;
+      Seg g;
+      bool ok = true;
+      uint32_t c = 0, cr = 0;  // key tiles, raw tiles
+      auto widen = [&](bool v) -> bool {
+        const int NS = v ? VS : KS, st = c % NS, rs = cr % RS;
+        uint64_t* full = v ? &B->v_full[st] : &B->k_full[st];
+        uint64_t* empty = v ? &B->v_empty[st] : &B->k_empty[st];
+        bool w = wait_ok(&B->raw_full[rs], (cr / RS) & 1, B, p.dev_err);
+        const uint8_t* src = smem + L::kRawOff + rs * L::kRaw;
+        uint8_t* dst = smem + (v ? L::kVOff : L::kKOff) + st * L::kOp;
+        w = w && (c < (uint32_t)NS || wait_ok(empty, (c / NS - 1) & 1, B, p.dev_err));
+        if (!__all_sync(0xffffffffu, w)) return false;
+#pragma unroll
+        for (int m = 0; m < kCh; ++m) {
+          const int idx = ct + 128 * m, key = idx / kCh, cc = idx % kCh;
+          const uint4 x = *reinterpret_cast<const uint4*>(src + raw_off<D>(key, cc));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (v) {
+              y[2 * e] = e4m3x2_to_f16x2_div256(xw[e], 0x4140u);
+              y[2 * e + 1] = e4m3x2_to_f16x2_div256(xw[e], 0x4342u);
+            } else {
+              y[2 * e] = e4m3x2_to_f16x2(xw[e] & 0xffffu);
+              y[2 * e + 1] = e4m3x2_to_f16x2(xw[e] >> 16);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc + 1)) =
+              make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        mbar_arrive(&B->raw_empty[rs]);
+        tc::fence_async_smem();
+        mbar_arrive(full);
+        ++cr;
+        return true;
+      };
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+        __syncwarp();
+        if (lane == 0) rd.done(B);
+        for (int t = g.t0; t < g.t1 && ok; ++t) {
+          ok = widen(false) && widen(true);
+          ++c;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    tc::regs_inc<L::kSoftRegs>();
+    const int x = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row = TMEM lane
+    const int ri = r / G, rh = r - ri * G;  // its node within the tile, its head
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lanes, tO = tmem + 256 + lanes;
+    // rows without a node, and sequences without context: zeros
+    if (rg == 0)
+      for (int s = blockIdx.x / nrg; s < p.num_seqs; s += gridDim.x / nrg) {
+        const int from = seq_ctx(p, s) > 0 ? seq_nodes(p, s) : 0;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T16*>(p.out) +
+                                            (size_t)s * p.q_len * p.n_q * D);
+        for (int i = from * p.n_q * D / 8 + threadIdx.x; i < p.q_len * p.n_q * D / 8; i += 256)
+          o[i] = make_uint4(0, 0, 0, 0);
+      }
+    Reader rd;
+    Seg g;
+    int t = 0, n_mine = 0, n_segs = 0;
+    bool ok = true;
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+      __syncwarp();
+      if (lane == 0) rd.done(B);
+      const int nodes = tile_nodes(g, x);
+      if (nodes == 0) continue;  // (never when split)
+      const int seg = n_segs++;
+      const int node = (SPLIT ? 0 : 2 * rg + x) * QT + ri;
+      const bool valid = ri < nodes;  // (ri < QT: rows past QT G are not)
+      const bool live = q4 * 32 < nodes * G;
+      const size_t row = ((size_t)g.s * p.q_len + (valid ? node : 0)) * p.n_q + g.h * G + rh;
+      uint64_t mask = valid ? __ldg(&p.masks[(size_t)g.s * p.q_len + node]) : 0ull;
+      if (g.n < 64) mask &= (1ull << g.n) - 1ull;
+      float sl = p.scale_log2;
+      if constexpr (FP8) {
+        // the query row as f16: a bf16 row times 2^e, its scores times 2^-e
+        uint4 v[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T16*>(p.q) + row * D);
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch) v[ch] = valid ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+        if constexpr (BF16) {
+          uint32_t mag = 0;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch)
+            mag = max(max(mag, max(bf16x2_max_mag(v[ch].x), bf16x2_max_mag(v[ch].y))),
+                      max(bf16x2_max_mag(v[ch].z), bf16x2_max_mag(v[ch].w)));
+          const int e = f16_row_shift(mag);
+          const float up = exp2i(e);
+          sl *= exp2i(-e);
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch)
+            v[ch] = make_uint4(
+                bf16x2_to_f16x2_scaled(v[ch].x, up), bf16x2_to_f16x2_scaled(v[ch].y, up),
+                bf16x2_to_f16x2_scaled(v[ch].z, up), bf16x2_to_f16x2_scaled(v[ch].w, up));
+        }
+        if (!SPLIT || x == 0) {
+          if (seg > 0)
+            ok = __all_sync(0xffffffffu, wait_ok(&B->q_empty[x], (seg - 1) & 1, B, p.dev_err));
+          if (!ok) break;
+          uint8_t* d = smem + L::kQOff + x * L::kOp;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch)
+            *reinterpret_cast<uint4*>(d + op_off(r, ch)) = v[ch];
+          tc::fence_async_smem();
+          mbar_arrive(&B->q_full[x]);
+        }
+      }
+      const int P = g.ctx - g.n;  // keys before the tree; may be negative
+      float m = -INFINITY, l = 0.f;
+      const int nt = g.t1 - g.t0;
+      bool any = false;
+      for (int ti = SPLIT ? x : 0; ti < nt; ti += SPLIT ? 2 : 1, ++t) {
+        ok = __all_sync(0xffffffffu, wait_ok(&B->s_full[x], t & 1, B, p.dev_err));
+        if (!ok) break;
+        if (live) {  // rows without a node: nothing reads their P or O
+          tc::fence_after();
+          const int key = (g.t0 + ti) * kTileN;
+          const bool full = key + kTileN <= P && p.scale_log2 > 0.f;
+          uint32_t vis[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = seen_bits(key + 32 * w, P, mask);
+          float s[kTileN];
+          attn::load_scores(tS, s);
+          const float mx = attn::tile_max(s, full, vis, sl);
+          const float mn = fmaxf(m, mx);
+          const bool grow = mn > m + attn::kRescaleLog2;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = exp2f(m - mn);  // 0 on the row's first keys
+            l *= alpha;
+            m = mn;
+          }
+          // S of this tile is done, so O += P V of the one before is too
+          if (any && __any_sync(0xffffffffu, grow)) attn::rescale_o(tO + x * 128, D, alpha);
+          // a row that has seen no key yet: its weights are 0
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          uint32_t pk[32];
+          l += attn::tile_weights<kOpBf16, 0>(s, 0, full, sl, neg_m, pk);
+          tc::st32x32b_x32(tS, pk);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&B->p_half[x]);
+          l += attn::tile_weights<kOpBf16, 0>(s, 1, full, sl, neg_m, pk);
+          tc::st32x32b_x32(tS + 32, pk);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&B->p_full[x]);
+        } else {
+          mbar_arrive(&B->p_half[x]);
+          mbar_arrive(&B->p_full[x]);
+        }
+        any = true;
+      }
+      if (!ok) break;
+      // ------------------------------------------------ segment epilogue
+      if (any) {
+        ok = __all_sync(0xffffffffu, wait_ok(&B->o_full[x], n_mine & 1, B, p.dev_err));
+        if (!ok) break;
+        ++n_mine;
+      }
+      // columns c0 .. c0 + W - 1 of the row: w0 O_A + w1 O_B when split (the
+      // other tile's (m, l) come through shared memory), else w0 O_X
+      constexpr int W = SPLIT ? D / 2 : D;
+      const int c0 = SPLIT ? x * (D / 2) : 0;
+      float w0 = 1.f, w1 = 0.f;
+      if constexpr (SPLIT) {
+        float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + (seg & 1) * 256 + r;
+        red[x * 128] = make_float2(m, l);
+        tc::fence_before();
+        mbar_arrive(&B->red[x]);
+        ok = __all_sync(0xffffffffu, wait_ok(&B->red[x ^ 1], seg & 1, B, p.dev_err));
+        if (!ok) break;
+        const float2 a = red[0], b = red[128];
+        m = fmaxf(a.x, b.x);
+        w0 = a.x == -INFINITY ? 0.f : exp2f(a.x - m);
+        w1 = b.x == -INFINITY ? 0.f : exp2f(b.x - m);
+        l = w0 * a.y + w1 * b.y;
+      } else if (m == -INFINITY) {
+        w0 = 0.f;
+      }
+      tc::fence_after();
+      const size_t slot = g.slot < 0 ? 0
+                                     : ((size_t)blockIdx.x * 2 + g.slot) * (SPLIT ? 128 : 256) +
+                                           (SPLIT ? 0 : x * 128) + r;
+      if (g.slot < 0) {
+        const float inv = l > 0.f ? p.out_mul / l : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+      } else if (valid && (!SPLIT || x == 0)) {
+        p.ws_ml[slot] = make_float2(m, l);
+      }
+      T16* out = static_cast<T16*>(p.out) + row * D + c0;
+      float* wo = p.ws_o + slot * D + c0;
+      if (live) {
+#pragma unroll 1
+        for (int cc = 0; cc < W; cc += 32) {
+          uint32_t o[32], ob[SPLIT ? 32 : 1];
+          tc::ld32x32b_x32(tO + (SPLIT ? 0 : x * 128) + c0 + cc, o);
+          if constexpr (SPLIT) tc::ld32x32b_x32(tO + 128 + c0 + cc, ob);
+          tc::wait_ld();
+          if (valid) {
+            // a tile without weight may hold anything
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              y[e] = w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0;
+              if constexpr (SPLIT) y[e] += w1 == 0.f ? 0.f : __uint_as_float(ob[e]) * w1;
+            }
+            if (g.slot < 0) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(out + cc + e) =
+                    make_uint4(pack2<BF16>(y[e], y[e + 1]), pack2<BF16>(y[e + 2], y[e + 3]),
+                               pack2<BF16>(y[e + 4], y[e + 5]), pack2<BF16>(y[e + 6], y[e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(wo + cc + e) =
+                    make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc::fence_before();
+      if constexpr (SPLIT) {
+        mbar_arrive(&B->o_free[0]);
+        mbar_arrive(&B->o_free[1]);
+      } else {
+        mbar_arrive(&B->o_free[x]);
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::dealloc(tmem, kTmemCols);
+  }
+}
+
+// Combines the segments of the units split between shares.  CTA (c, y) looks
+// at the boundary between shares c and c + 1: if it cuts a unit whose first
+// step lies in share c, this CTA merges 32 of the unit's rows, a warp a row,
+// from the shares' slots in order.  Every other row was written whole.
+template <typename OutT, int D, bool SPLIT>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+  __shared__ int sh_s, sh_h;
+  __shared__ long long sh_u, sh_end, sh_T;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long C = gridDim.x, c = blockIdx.x;
+  // finding the unit reads only the lengths, so it overlaps the attention
+  // kernel (this grid is its programmatic dependent); pdl_wait comes before
+  // the workspace is read
+  if (warp == 0) {
+    int s = -1, h = 0;
+    long long u = 0, end = 0, T = 0;
+    if (c + 1 < C) {
+      T = total_weight(p, lane, false);
+      const long long X = share_start(T, c + 1, C);
+      int s0, w;
+      long long gs;
+      if (X < T && locate(p, X, lane, s0, gs, w)) {
+        h = (int)((X - gs) / w);
+        u = gs + (long long)h * w + kSegCost;
+        end = u + w - kSegCost;
+        if (u < X && u >= share_start(T, c, C)) s = s0;
+      }
+    }
+    if (lane == 0) {
+      sh_s = s;
+      sh_h = h;
+      sh_u = u;
+      sh_end = end;
+      sh_T = T;
+    }
+  }
+  __syncthreads();
+  pdl_wait();  // the attention kernel's results
+  if (sh_s < 0) return;
+  const int G = p.group, QT = kTileM / G, n = seq_nodes(p, sh_s);
+  const long long T = sh_T, end = sh_end;
+  constexpr int RW = SPLIT ? 128 : 256, V = D / 32;  // rows of a slot, floats a lane
+  for (int k = warp; k < 32; k += 8) {
+    const int row = blockIdx.y * 32 + k;  // of the CTAs side by side: RW each
+    const int rg = row / RW, in = row % RW, r = in % kTileM;
+    const int node = (row / kTileM) * QT + r / G;
+    if (r / G >= QT || node >= n) continue;
+    float M = -INFINITY, Ls = 0.f, acc[V] = {};
+    for (long long cc = c; cc < C && share_start(T, cc, C) < end; ++cc) {
+      const long long lo = share_start(T, cc, C), hi = share_start(T, cc + 1, C);
+      if ((lo > sh_u ? lo : sh_u) >= (hi < end ? hi : end)) continue;  // none of its steps
+      const size_t slot = ((cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
+      const float2 v = p.ws_ml[slot];
+      if (v.x == -INFINITY) continue;
+      const float mn = fmaxf(M, v.x), wa = exp2f(M - mn), wb = exp2f(v.x - mn);
+      const float* o = p.ws_o + slot * D + lane * V;
+      Ls = Ls * wa + v.y * wb;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = acc[e] * wa + o[e] * wb;
+      M = mn;
+    }
+    const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
+    constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        static_cast<OutT*>(p.out) +
+        (((size_t)sh_s * p.q_len + node) * p.n_q + sh_h * G + r % G) * D + lane * V);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf>(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <bool BF16, int D, bool FP8, bool SPLIT>
+cudaError_t launch_t(const TreeParams& p, const CUtensorMap* tmq, const CUtensorMap* tmk,
+                     const CUtensorMap* tmv, cudaStream_t st) {
+  using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using L = Lay<D, FP8, SPLIT>;
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<BF16, D, FP8, SPLIT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  int shares = device_sms() < kTreeCtas ? device_sms() : kTreeCtas;
+  shares /= p.row_groups;
+  tree_kernel<BF16, D, FP8, SPLIT>
+      <<<shares * p.row_groups, L::kThreads, L::kSmem, st>>>(p, *tmq, *tmk, *tmv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)shares, (SPLIT ? 128 : 256) / 32 * p.row_groups);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T16, D, SPLIT>, p);
+}
+
+template <bool BF16, int D>
+cudaError_t launch_d(const TreeParams& p, bool fp8, const CUtensorMap* tmq, const CUtensorMap* tmk,
+                     const CUtensorMap* tmv, cudaStream_t st) {
+  const bool split = p.step_keys == 2 * kTileN;
+  if (fp8)
+    return split ? launch_t<BF16, D, true, true>(p, tmq, tmk, tmv, st)
+                 : launch_t<BF16, D, true, false>(p, tmq, tmk, tmv, st);
+  return split ? launch_t<BF16, D, false, true>(p, tmq, tmk, tmv, st)
+               : launch_t<BF16, D, false, false>(p, tmq, tmk, tmv, st);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const TreeParams& p, int D, bool bf16, bool fp8, cudaStream_t st) {
+size_t tree_ws_bytes(int q_len, int group, int D) {
+  const int tiles = (q_len + kTileM / group - 1) / (kTileM / group);
+  const size_t rows = (size_t)kTreeCtas * 2 * (tiles == 1 ? 128 : 256);
+  return rows * D * sizeof(float) + rows * sizeof(float2);
+}
+
+cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspace,
+                        const CUtensorMap* tmq, const CUtensorMap* tmk, const CUtensorMap* tmv,
+                        cudaStream_t st) {
   if (p.num_seqs == 0) return cudaSuccess;
-  if (bf16)
-    return fp8 ? launch_t<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
-               : launch_t<__nv_bfloat16, __nv_bfloat16>(p, D, st);
-  return fp8 ? launch_t<__half, __nv_fp8_e4m3>(p, D, st) : launch_t<__half, __half>(p, D, st);
+  const int qt = kTileM / p.group, tiles = (p.q_len + qt - 1) / qt;
+  p.row_groups = tiles > 2 ? 2 : 1;
+  p.step_keys = tiles == 1 ? 2 * kTileN : kTileN;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (size_t)kTreeCtas * 2 * (tiles == 1 ? 128 : 256) * D);
+  if (D == 128)
+    return bf16 ? launch_d<true, 128>(p, fp8, tmq, tmk, tmv, st)
+                : launch_d<false, 128>(p, fp8, tmq, tmk, tmv, st);
+  return bf16 ? launch_d<true, 64>(p, fp8, tmq, tmk, tmv, st)
+              : launch_d<false, 64>(p, fp8, tmq, tmk, tmv, st);
 }
 
 }  // namespace pa
