@@ -103,6 +103,37 @@ __device__ __forceinline__ float tile_max(float (&x)[kTileN], bool full, const u
   return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 }
 
+// The same 64 keys at a time, for kernels whose threads cannot hold 128 scores:
+// the maximum is taken on one reading of S, the weights on another.
+__device__ __forceinline__ void load_half(uint32_t ts, int h, bool full, const uint32_t (&vis)[4],
+                                          float sl, float (&x)[64]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  tc::ld32x32b_x32(ts + 64 * h, r);
+  tc::ld32x32b_x32(ts + 64 * h + 32, r + 32);
+  tc::wait_ld();
+  if (!full) {
+#pragma unroll
+    for (int e = 0; e < 64; ++e)
+      x[e] = (vis[2 * h + (e >> 5)] >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
+  }
+}
+__device__ __forceinline__ float tile_max_halves(uint32_t ts, bool full, const uint32_t (&vis)[4],
+                                                 float sl) {
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float x[64];
+    const uint32_t v[4] = {h ? vis[2] : vis[0], h ? vis[3] : vis[1], 0u, 0u};
+    load_half(ts + 64 * h, 0, full, v, sl, x);
+#pragma unroll
+    for (int e = 0; e < 64; e += 8)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(x[e + 2 * c], x[e + 2 * c + 1]));
+  }
+  const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  return full ? mx * sl : mx;
+}
+
 // Multiplies `cols` columns of the row's O by alpha.
 __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
 #pragma unroll 1
@@ -120,7 +151,7 @@ __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
 // Weights of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns their
 // fp32 sum.  Of every 8 pairs without a mask kPoly go through exp2_poly2.
 template <bool BF16, int kPoly>
-__device__ __forceinline__ float tile_weights(const float (&x)[kTileN], int h, bool full, float sl,
+__device__ __forceinline__ float tile_weights(const float* x, int h, bool full, float sl,
                                               float neg_m, uint32_t (&pk)[32]) {
   uint64_t s[2] = {0ull, 0ull};
   const uint64_t nm = f2(neg_m, neg_m), s2 = f2(sl, sl);

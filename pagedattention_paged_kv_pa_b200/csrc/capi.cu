@@ -527,7 +527,8 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
   p.tree_lens = tree_lens;
   p.masks = masks;
   p.dev_err = dev_err;
-  p.scale_log2 = scale * kLog2e * (fp8 ? k_scale : 1.f);
+  // the kernel widens E4M3 codes to f16 as code x 2^-8
+  p.scale_log2 = scale * kLog2e * (fp8 ? k_scale * kFp8VUnscale : 1.f);
   p.out_mul = fp8 ? v_scale * kFp8VUnscale : 1.f;
   p.n_q = n_q_heads;
   p.n_kv = n_kv_heads;

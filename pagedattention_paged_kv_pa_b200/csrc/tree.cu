@@ -31,9 +31,9 @@
 // TMEM and issues the MMAs, warp 9 loads Q and K, warp 10 V (16-token blocks
 // by TMA through the block table; rows of the block a context ends in are
 // copied, rows past it and blocks with a bad id zeroed by the warp itself),
-// warp 11 walks the share.  E4M3 caches: warp 9 brings the raw K and V rows
-// into a ring of raw tiles and warps 12-15 widen them to the f16 operands (K
-// exactly, V as code x 2^-8, exactly too, undone by the output scale); the
+// warp 11 walks the share.  E4M3 caches: warps 9 and 10 bring raw rows into
+// rings of raw tiles, and warps 12-15 widen K, 16-19 V to the f16 operands
+// (code x 2^-8, exact, undone by the score and output scales); the
 // softmax threads write their query rows, scaled by a power of two into f16's
 // range when they are bf16, and P is f16.  Every wait is bounded; a role that
 // gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its loads
@@ -63,21 +63,21 @@ struct Lay {
   static constexpr int kScale = 128 / D;
   static constexpr int kKS = (FP8 ? 2 : 3) * kScale;
   static constexpr int kVS = (FP8 && !SPLIT && D == 128 ? 1 : 2) * kScale;
-  static constexpr int kRS = FP8 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kRS = FP8 ? 2 * kScale : 0;  // raw K stages, and raw V stages
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kQ * kOp;
   static constexpr int kVOff = kKOff + kKS * kOp;
   static constexpr int kRawOff = kVOff + kVS * kOp;
-  static constexpr int kRedOff = kRawOff + kRS * kRaw;  // [2][2][128] float2
-  static constexpr int kBarOff = kRedOff + (SPLIT ? 4096 : 0);
-  static constexpr int kSmem = kBarOff + 1024 + 1024;
+  static constexpr int kRedOff = kRawOff + 2 * kRS * kRaw;  // [2][128] float2
+  static constexpr int kBarOff = kRedOff + (SPLIT ? 2048 : 0);
+  static constexpr int kSmem = kBarOff + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static constexpr int kThreads = FP8 ? 512 : 384;
-  // registers: 512 x 128 = 256 x 176 + 256 x 80, or 384 x 168 = 256 x 200 +
-  // 128 x 96 + 1,024
-  static constexpr int kSoftRegs = FP8 ? 176 : 200, kOtherRegs = FP8 ? 80 : 96;
-  // readers of a segment: 8 softmax warps, MMA, loads (K, V), 4 converters
-  static constexpr uint32_t kReaders = FP8 ? 14 : 11;
+  static constexpr int kThreads = FP8 ? 640 : 384;
+  // registers: 640 x 96 = 61,440 = 256 x 128 + 384 x 72 + 1,024, or 384 x 168 =
+  // 64,512 = 256 x 200 + 128 x 96 + 1,024
+  static constexpr int kSoftRegs = FP8 ? 128 : 200, kOtherRegs = FP8 ? 72 : 96;
+  // readers of a segment: 8 softmax warps, MMA, K and V loads, 8 converters
+  static constexpr uint32_t kReaders = FP8 ? 19 : 11;
 };
 
 struct Seg {
@@ -88,7 +88,7 @@ struct Seg {
 };
 
 struct Bars {
-  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], raw_full[4], raw_empty[4];
+  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], raw_full[2][4], raw_empty[2][4];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], red[2];
   uint64_t done;
@@ -156,10 +156,18 @@ __device__ long long total_weight(const TreeParams& p, int lane, bool report) {
   for (int m = 16; m >= 1; m >>= 1) part += __shfl_xor_sync(0xffffffffu, part, m);
   return part * p.n_kv;
 }
-// floor(c T / C) without overflow
-__device__ __forceinline__ long long share_start(long long T, long long c, long long C) {
-  return (T / C) * c + (T % C) * c / C;
-}
+// The shares: share c starts at floor(c T / C) = c floor(T / C) + floor(c (T mod
+// C) / C).  With fewer positions than CTAs, C is T, so that none is empty.
+struct Shares {
+  long long each;
+  int C, rest;
+  __device__ Shares(long long T, int ctas) {
+    C = T < ctas ? max((int)T, 1) : ctas;
+    each = T / C;
+    rest = (int)(T - each * C);
+  }
+  __device__ __forceinline__ long long start(int c) const { return each * c + c * rest / C; }
+};
 // The sequence whose span [gs, gs + n_kv w) of positions holds X, by one warp.
 __device__ bool locate(const TreeParams& p, long long X, int lane, int& s_out, long long& gs_out,
                        int& w_out) {
@@ -200,17 +208,23 @@ __device__ __forceinline__ uint32_t raw_off(int row, int chunk) {
   return D == 128 ? swz128(row * 128 + chunk * 16) : swz64(row * 64 + chunk * 16);
 }
 
+// The block id of lane m < 8's block m of tile t (-1 past the context).
+__device__ __forceinline__ int block_id(const TreeParams& p, const Seg& g, int t, int lane) {
+  const int blk = t * 8 + lane;
+  return lane < 8 && blk * 16 < g.ctx ? __ldg(&p.block_tables[(size_t)g.s * p.max_blocks + blk])
+                                      : -1;
+}
+
 // Loads tile t of a (sequence, kv head) into `dst`, by one warp: whole blocks
 // of the context by TMA, the other rows written here.
 template <int D, bool FP8>
 __device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int t, uint8_t* dst,
                                           const CUtensorMap* map, const uint8_t* pool,
-                                          uint64_t* full, int lane, bool report,
+                                          uint64_t* full, int lane, int phys, bool report,
                                           uint64_t policy) {
   constexpr int kRow = FP8 ? D : 2 * D;  // bytes of a row
   const int blk = t * 8 + lane;
   const bool in_ctx = lane < 8 && blk * 16 < g.ctx;
-  const int phys = in_ctx ? __ldg(&p.block_tables[(size_t)g.s * p.max_blocks + blk]) : -1;
   const bool in_range = phys >= 0 && phys < p.num_blocks;
   if (report && in_ctx && !in_range) flag_error(p.dev_err, PA_DEVERR_BLOCK_ID);
   const bool whole = in_ctx && in_range && blk * 16 + 16 <= g.ctx;
@@ -256,15 +270,14 @@ __device__ __forceinline__ uint32_t seen_bits(int first, int P, uint64_t mask) {
 }
 
 template <bool BF16, int D, bool FP8, bool SPLIT>
-__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
+__global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
     tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   using L = Lay<D, FP8, SPLIT>;
   constexpr bool kOpBf16 = BF16 && !FP8;  // the operands' type
   constexpr int KS = L::kKS, VS = L::kVS, RS = FP8 ? L::kRS : 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars* B = reinterpret_cast<Bars*>(smem + L::kBarOff);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -286,8 +299,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       mbar_init(&B->v_empty[s], 1);
     }
     for (int s = 0; s < RS; ++s) {
-      mbar_init(&B->raw_full[s], 1);
-      mbar_init(&B->raw_empty[s], 128);
+      for (int v = 0; v < 2; ++v) {
+        mbar_init(&B->raw_full[v][s], 1);
+        mbar_init(&B->raw_empty[v][s], 128);
+      }
     }
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&B->seg_full[s], 1);
@@ -430,40 +445,39 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         __syncwarp();
         mbar_wait(&B->done, 0);
       }
-    } else if (warp == kKWarp || (!FP8 && warp == kVWarp)) {
+    } else if (warp == kKWarp || warp == kVWarp) {
       // ---------------------------------------------------------------- loads
-      // 16-bit caches: K (with Q) and V by a warp each; E4M3: K and V of each
-      // tile in turn through one ring of raw tiles
       const bool vop = warp == kVWarp;
       const int NS = FP8 ? RS : (vop ? VS : KS);
-      uint64_t* full = FP8 ? B->raw_full : (vop ? B->v_full : B->k_full);
-      uint64_t* empty = FP8 ? B->raw_empty : (vop ? B->v_empty : B->k_empty);
-      uint8_t* ring = smem + (FP8 ? L::kRawOff : (vop ? L::kVOff : L::kKOff));
+      uint64_t* full = FP8 ? B->raw_full[vop] : (vop ? B->v_full : B->k_full);
+      uint64_t* empty = FP8 ? B->raw_empty[vop] : (vop ? B->v_empty : B->k_empty);
       constexpr int kStage = FP8 ? L::kRaw : L::kOp;
-      const uint64_t policy = l2_policy_evict_first();  // K/V are read once
+      uint8_t* ring = smem + (FP8 ? L::kRawOff + (vop ? RS * kStage : 0)
+                                  : (vop ? L::kVOff : L::kKOff));
+      const uint8_t* pool = static_cast<const uint8_t*>(vop ? p.v_pool : p.k_pool);
+      const CUtensorMap* map = vop ? &tmv : &tmk;
+      // K/V are read once, unless by the CTA alongside too
+      const uint64_t policy = l2_policy_evict_first();
       Reader rd;
       Seg g;
       bool ok = true;
       uint32_t c = 0;
       int nq[2] = {0, 0};
-      auto tile = [&](int t, bool v) -> bool {
-        const int st = c % NS;
-        const bool w = c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
-        if (!__all_sync(0xffffffffu, w)) return false;
-        load_tile<D, FP8>(p, g, t, ring + st * kStage, v ? &tmv : &tmk,
-                          static_cast<const uint8_t*>(v ? p.v_pool : p.k_pool), &full[st], lane,
-                          !v, policy);
-        ++c;
-        return true;
-      };
       while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
-        for (int t = g.t0; t < g.t1 && ok; ++t) {
-          ok = tile(t, vop);
-          if (FP8) {
-            ok = ok && tile(t, true);
-          } else if (!vop && t == g.t0) {
+        int id = block_id(p, g, g.t0, lane);
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++c) {
+          // the next tile's block ids arrive while this tile waits for a stage
+          const int id_next = t + 1 < g.t1 ? block_id(p, g, t + 1, lane) : -1;
+          const int st = c % NS;
+          const bool w = c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+          ok = __all_sync(0xffffffffu, w);
+          if (!ok) break;
+          load_tile<D, FP8>(p, g, t, ring + st * kStage, map, pool, &full[st], lane, id, !vop,
+                            policy);
+          id = id_next;
+          if (!FP8 && !vop && t == g.t0) {
 #pragma unroll
             for (int x = 0; x < L::kQ; ++x) {
               if (!ok || tile_nodes(g, x) == 0) continue;
@@ -495,12 +509,12 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
     } else if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
-      const long long T = total_weight(p, lane, blockIdx.x == 0);
-      const long long C = gridDim.x / nrg, sc = blockIdx.x / nrg;
-      const long long gbeg = share_start(T, sc, C), gend = share_start(T, sc + 1, C);
+      const Shares sh(total_weight(p, lane, blockIdx.x == 0), gridDim.x / nrg);
+      const int sc = blockIdx.x / nrg;
+      const long long gbeg = sh.start(sc), gend = sh.start(sc + 1);
       int s = 0, w = 0, h = 0, step = 0;
       long long gs = 0;
-      bool more = gbeg < gend && locate(p, gbeg, lane, s, gs, w);
+      bool more = sc < sh.C && gbeg < gend && locate(p, gbeg, lane, s, gs, w);
       if (more) {
         h = (int)((gbeg - gs) / w);
         step = max(0, (int)((gbeg - gs) % w) - kSegCost);
@@ -552,54 +566,50 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         if (g.s < 0) break;
       }
     } else if (FP8 && warp >= 12) {
-      // ----------------------------------------------------------- converters
-      const int ct = threadIdx.x - 384;  // 0 .. 127
-      constexpr int kCh = D / 16;        // 16-code chunks of a row
+      // ------------------------------------- converters: 4 warps for K, 4 for V
+      const bool vop = warp >= 16;
+      const int ct = threadIdx.x - (vop ? 512 : 384);  // 0 .. 127
+      const int NS = vop ? VS : KS;
+      uint64_t* full = vop ? B->v_full : B->k_full;
+      uint64_t* empty = vop ? B->v_empty : B->k_empty;
+      constexpr int kCh = D / 16;  // 16-code chunks of a row
       Reader rd;
       Seg g;
       bool ok = true;
-      uint32_t c = 0, cr = 0;  // key tiles, raw tiles
-      auto widen = [&](bool v) -> bool {
-        const int NS = v ? VS : KS, st = c % NS, rs = cr % RS;
-        uint64_t* full = v ? &B->v_full[st] : &B->k_full[st];
-        uint64_t* empty = v ? &B->v_empty[st] : &B->k_empty[st];
-        bool w = wait_ok(&B->raw_full[rs], (cr / RS) & 1, B, p.dev_err);
-        const uint8_t* src = smem + L::kRawOff + rs * L::kRaw;
-        uint8_t* dst = smem + (v ? L::kVOff : L::kKOff) + st * L::kOp;
-        w = w && (c < (uint32_t)NS || wait_ok(empty, (c / NS - 1) & 1, B, p.dev_err));
-        if (!__all_sync(0xffffffffu, w)) return false;
-#pragma unroll
-        for (int m = 0; m < kCh; ++m) {
-          const int idx = ct + 128 * m, key = idx / kCh, cc = idx % kCh;
-          const uint4 x = *reinterpret_cast<const uint4*>(src + raw_off<D>(key, cc));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (v) {
-              y[2 * e] = e4m3x2_to_f16x2_div256(xw[e], 0x4140u);
-              y[2 * e + 1] = e4m3x2_to_f16x2_div256(xw[e], 0x4342u);
-            } else {
-              y[2 * e] = e4m3x2_to_f16x2(xw[e] & 0xffffu);
-              y[2 * e + 1] = e4m3x2_to_f16x2(xw[e] >> 16);
-            }
-          }
-          *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc + 1)) =
-              make_uint4(y[4], y[5], y[6], y[7]);
-        }
-        mbar_arrive(&B->raw_empty[rs]);
-        tc::fence_async_smem();
-        mbar_arrive(full);
-        ++cr;
-        return true;
-      };
+      uint32_t c = 0;
       while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
-        for (int t = g.t0; t < g.t1 && ok; ++t) {
-          ok = widen(false) && widen(true);
-          ++c;
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++c) {
+          const int st = c % NS, rs = c % RS;
+          bool w = wait_ok(&B->raw_full[vop][rs], (c / RS) & 1, B, p.dev_err);
+          w = w && (c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err));
+          ok = __all_sync(0xffffffffu, w);
+          if (!ok) break;
+          const uint8_t* src = smem + L::kRawOff + ((vop ? RS : 0) + rs) * L::kRaw;
+          uint8_t* dst = smem + (vop ? L::kVOff : L::kKOff) + st * L::kOp;
+#pragma unroll
+          for (int m = 0; m < kCh; ++m) {
+            // 8 lanes take 8 rows of one chunk, then the next chunk: their
+            // 16-byte stores fall into different banks (the swizzle turns with
+            // the row)
+            const int key = (ct & 7) + 8 * (ct / (8 * kCh)) + (128 / kCh) * m, cc = (ct >> 3) % kCh;
+            const uint4 x = *reinterpret_cast<const uint4*>(src + raw_off<D>(key, cc));
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = e4m3x2_to_f16x2_div256(xw[e], 0x4140u);
+              y[2 * e + 1] = e4m3x2_to_f16x2_div256(xw[e], 0x4342u);
+            }
+            *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + op_off(key, 2 * cc + 1)) =
+                make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          mbar_arrive(&B->raw_empty[vop][rs]);
+          tc::fence_async_smem();
+          mbar_arrive(&full[st]);
         }
       }
     }
@@ -684,9 +694,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           uint32_t vis[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] = seen_bits(key + 32 * w, P, mask);
-          float s[kTileN];
-          attn::load_scores(tS, s);
-          const float mx = attn::tile_max(s, full, vis, sl);
+          float s[FP8 ? 64 : kTileN];
+          float mx;
+          if constexpr (FP8) {
+            mx = attn::tile_max_halves(tS, full, vis, sl);
+          } else {
+            attn::load_scores(tS, s);
+            mx = attn::tile_max(s, full, vis, sl);
+          }
           const float mn = fmaxf(m, mx);
           const bool grow = mn > m + attn::kRescaleLog2;
           float alpha = 1.f;
@@ -700,12 +715,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           // a row that has seen no key yet: its weights are 0
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
+          if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
           l += attn::tile_weights<kOpBf16, 0>(s, 0, full, sl, neg_m, pk);
           tc::st32x32b_x32(tS, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
-          l += attn::tile_weights<kOpBf16, 0>(s, 1, full, sl, neg_m, pk);
+          if constexpr (FP8) attn::load_half(tS, 1, full, vis, sl, s);
+          l += attn::tile_weights<kOpBf16, 0>(s, FP8 ? 0 : 1, full, sl, neg_m, pk);
           tc::st32x32b_x32(tS + 32, pk);
           tc::wait_st();
           tc::fence_before();
@@ -729,7 +746,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const int c0 = SPLIT ? x * (D / 2) : 0;
       float w0 = 1.f, w1 = 0.f;
       if constexpr (SPLIT) {
-        float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + (seg & 1) * 256 + r;
+        float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + r;
+        // (the segment before was read out by both)
+        if (seg > 0)
+          ok = __all_sync(0xffffffffu, wait_ok(&B->o_free[0], (seg - 1) & 1, B, p.dev_err));
+        if (!ok) break;
         red[x * 128] = make_float2(m, l);
         tc::fence_before();
         mbar_arrive(&B->red[x]);
@@ -810,42 +831,44 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
 // step lies in share c, this CTA merges 32 of the unit's rows, a warp a row,
 // from the shares' slots in order.  Every other row was written whole.
 template <typename OutT, int D, bool SPLIT>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
-  __shared__ int sh_s, sh_h;
-  __shared__ long long sh_u, sh_end, sh_T;
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int ctas) {
+  __shared__ int sh_s, sh_h, sh_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long C = gridDim.x, c = blockIdx.x;
+  const int c = blockIdx.x;
   // finding the unit reads only the lengths, so it overlaps the attention
   // kernel (this grid is its programmatic dependent); pdl_wait comes before
   // the workspace is read
   if (warp == 0) {
-    int s = -1, h = 0;
-    long long u = 0, end = 0, T = 0;
-    if (c + 1 < C) {
-      T = total_weight(p, lane, false);
-      const long long X = share_start(T, c + 1, C);
+    int s = -1, h = 0, last = c;
+    const Shares sh(total_weight(p, lane, false), ctas);
+    if (c + 1 < sh.C) {
+      const long long X = sh.start(c + 1);
       int s0, w;
       long long gs;
-      if (X < T && locate(p, X, lane, s0, gs, w)) {
+      if (locate(p, X, lane, s0, gs, w)) {
         h = (int)((X - gs) / w);
-        u = gs + (long long)h * w + kSegCost;
-        end = u + w - kSegCost;
-        if (u < X && u >= share_start(T, c, C)) s = s0;
+        const long long u = gs + (long long)h * w + kSegCost, end = u + w - kSegCost;
+        if (u < X && u >= sh.start(c)) {
+          s = s0;
+          // the last share with steps of the unit
+          for (int k = c + 1 + lane;; k += 32) {
+            const uint32_t in = __ballot_sync(0xffffffffu, k < sh.C && sh.start(k) < end);
+            last += __popc(in);
+            if (in != 0xffffffffu) break;
+          }
+        }
       }
     }
     if (lane == 0) {
       sh_s = s;
       sh_h = h;
-      sh_u = u;
-      sh_end = end;
-      sh_T = T;
+      sh_last = last;
     }
   }
   __syncthreads();
   pdl_wait();  // the attention kernel's results
   if (sh_s < 0) return;
-  const int G = p.group, QT = kTileM / G, n = seq_nodes(p, sh_s);
-  const long long T = sh_T, end = sh_end;
+  const int G = p.group, QT = kTileM / G, n = seq_nodes(p, sh_s), last = sh_last;
   constexpr int RW = SPLIT ? 128 : 256, V = D / 32;  // rows of a slot, floats a lane
   for (int k = warp; k < 32; k += 8) {
     const int row = blockIdx.y * 32 + k;  // of the CTAs side by side: RW each
@@ -853,17 +876,19 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     const int node = (row / kTileM) * QT + r / G;
     if (r / G >= QT || node >= n) continue;
     float M = -INFINITY, Ls = 0.f, acc[V] = {};
-    for (long long cc = c; cc < C && share_start(T, cc, C) < end; ++cc) {
-      const long long lo = share_start(T, cc, C), hi = share_start(T, cc + 1, C);
-      if ((lo > sh_u ? lo : sh_u) >= (hi < end ? hi : end)) continue;  // none of its steps
-      const size_t slot = ((cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
+#pragma unroll 4
+    for (int cc = c; cc <= last; ++cc) {
+      const size_t slot = ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
       const float2 v = p.ws_ml[slot];
-      if (v.x == -INFINITY) continue;
-      const float mn = fmaxf(M, v.x), wa = exp2f(M - mn), wb = exp2f(v.x - mn);
       const float* o = p.ws_o + slot * D + lane * V;
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = o[e];
+      if (v.x == -INFINITY) continue;  // no key seen: y may hold anything
+      const float mn = fmaxf(M, v.x), wa = exp2f(M - mn), wb = exp2f(v.x - mn);
       Ls = Ls * wa + v.y * wb;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = acc[e] * wa + o[e] * wb;
+      for (int e = 0; e < V; ++e) acc[e] = acc[e] * wa + y[e] * wb;
       M = mn;
     }
     const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
@@ -899,7 +924,7 @@ cudaError_t launch_t(const TreeParams& p, const CUtensorMap* tmq, const CUtensor
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T16, D, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T16, D, SPLIT>, p, shares);
 }
 
 template <bool BF16, int D>
