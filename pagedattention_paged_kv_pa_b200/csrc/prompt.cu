@@ -484,34 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = qi < it.len;
       const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
       T16* out = static_cast<T16*>(p.out) +
-                 ((size_t)(it.start + (valid ? qi : 0)) * p.n_q + it.h0 + (r & ((1 << lhb) - 1))) * D;
+                 ((size_t)(it.start + qi) * p.n_q + it.h0 + (r & ((1 << lhb) - 1))) * D;
+      if (!valid) out = nullptr;
       tc::fence_after();
       if (live) {
 #pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t o[32];
-          tc::ld32x32b_x32(tO + cc, o);
-          tc::wait_ld();
-          if (cc + 32 == D) {
-            tc::fence_before();
-            mbar_arrive(&B->o_free[x]);
-          }
-          if (valid) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v;
-              uint32_t* w = &v.x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack2<BF16>(__uint_as_float(o[e + 2 * k]) * inv,
-                                   __uint_as_float(o[e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + cc + e) = v;
-            }
-          }
-        }
-      } else {
-        mbar_arrive(&B->o_free[x]);
+        for (int cc = 0; cc < D; cc += 64)
+          attn::store_rows<T16, false>(tO + cc, 0, out ? out + cc : nullptr, inv, 0.f);
+        tc::fence_before();
       }
+      mbar_arrive(&B->o_free[x]);
     }
   }
   tc::fence_before();

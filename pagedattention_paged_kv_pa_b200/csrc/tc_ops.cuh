@@ -11,7 +11,8 @@
 //   2 (t % 4) and 2 (t % 4) + 1 of lanes base + t / 4 (registers 0, 1) and
 //   base + 8 + t / 4 (registers 2, 3); each repetition (.xN) moves 8 columns
 //   to the right -- the fragment an m16n8 matrix instruction uses, so a row
-//   pair of bf16 values packs straight into stmatrix operands;
+//   pair of bf16 values packs straight into stmatrix operands; the base lane
+//   may be the first or the 16th of the warp's quadrant;
 // - an M = 128 accumulator keeps row r in TMEM lane r, and 32x32b gives thread
 //   t of warp w of a warpgroup lane 32 w + t: one whole row per thread.
 #pragma once

@@ -53,6 +53,7 @@ using attn::kTileN;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
 constexpr int kSegs = 4;  // segments scheduled ahead
 constexpr uint32_t kTmemCols = 512;  // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr int kMergeRows = 16;  // rows of a merge CTA
 constexpr int kSegCost = 1;  // a unit's fixed costs, in steps
 
 template <int D, bool FP8, bool SPLIT>
@@ -139,22 +140,26 @@ __device__ __forceinline__ int seq_steps(const TreeParams& p, int s) {
 }
 __device__ __forceinline__ int weight(int steps) { return steps > 0 ? steps + kSegCost : 0; }
 
-// T, by one warp; flags lengths out of range when `report`
-__device__ long long total_weight(const TreeParams& p, int lane, bool report) {
-  long long part = 0;
-  int err = 0;
-  for (int s = lane; s < p.num_seqs; s += 32) {
-    part += weight(seq_steps(p, s));
-    if (report) {
+// T, by one warp; `first` gets the weight of sequence `lane`; flags lengths out
+// of range when `report`
+__device__ long long total_weight(const TreeParams& p, int lane, bool report, int& first) {
+  long long part = first = lane < p.num_seqs ? weight(seq_steps(p, lane)) : 0;
+  for (int s = 32 + lane; s < p.num_seqs; s += 32) part += weight(seq_steps(p, s));
+  if (report) {
+    int err = 0;
+    for (int s = lane; s < p.num_seqs; s += 32) {
       const int n = p.tree_lens ? __ldg(&p.tree_lens[s]) : p.q_len;
       if (n < 0 || n > p.q_len) err |= PA_DEVERR_QUERY_LOC;
       if (__ldg(&p.context_lens[s]) > p.max_blocks * 16) err |= PA_DEVERR_BLOCK_ID;
     }
+    if (err) flag_error(p.dev_err, err);
   }
-  if (err) flag_error(p.dev_err, err);
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) part += __shfl_xor_sync(0xffffffffu, part, m);
   return part * p.n_kv;
+}
+__device__ __forceinline__ int quotient(long long a, int b) {
+  return a < 0x7fffffff ? (int)a / b : (int)(a / b);
 }
 // The shares: share c starts at floor(c T / C) = c floor(T / C) + floor(c (T mod
 // C) / C).  With fewer positions than CTAs, C is T, so that none is empty.
@@ -163,18 +168,18 @@ struct Shares {
   int C, rest;
   __device__ Shares(long long T, int ctas) {
     C = T < ctas ? max((int)T, 1) : ctas;
-    each = T / C;
+    each = T < 0x7fffffff ? (int)T / C : T / C;
     rest = (int)(T - each * C);
   }
   __device__ __forceinline__ long long start(int c) const { return each * c + c * rest / C; }
 };
 // The sequence whose span [gs, gs + n_kv w) of positions holds X, by one warp.
-__device__ bool locate(const TreeParams& p, long long X, int lane, int& s_out, long long& gs_out,
-                       int& w_out) {
+__device__ bool locate(const TreeParams& p, long long X, int lane, int first, int& s_out,
+                       long long& gs_out, int& w_out) {
   long long acc = 0;
   for (int base = 0; base < p.num_seqs; base += 32) {
     const int s = base + lane;
-    const int n = s < p.num_seqs ? weight(seq_steps(p, s)) : 0;
+    const int n = base == 0 ? first : (s < p.num_seqs ? weight(seq_steps(p, s)) : 0);
     int incl = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -509,15 +514,16 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
     } else if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
-      const Shares sh(total_weight(p, lane, blockIdx.x == 0), gridDim.x / nrg);
+      int first;
+      const Shares sh(total_weight(p, lane, blockIdx.x == 0, first), gridDim.x / nrg);
       const int sc = blockIdx.x / nrg;
       const long long gbeg = sh.start(sc), gend = sh.start(sc + 1);
       int s = 0, w = 0, h = 0, step = 0;
       long long gs = 0;
-      bool more = sc < sh.C && gbeg < gend && locate(p, gbeg, lane, s, gs, w);
+      bool more = sc < sh.C && gbeg < gend && locate(p, gbeg, lane, first, s, gs, w);
       if (more) {
-        h = (int)((gbeg - gs) / w);
-        step = max(0, (int)((gbeg - gs) % w) - kSegCost);
+        h = quotient(gbeg - gs, w);
+        step = max(0, (int)(gbeg - gs - (long long)h * w) - kSegCost);
       }
       for (int k = 0;;) {
         Seg g;
@@ -740,10 +746,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         if (!ok) break;
         ++n_mine;
       }
-      // columns c0 .. c0 + W - 1 of the row: w0 O_A + w1 O_B when split (the
+      // the row's columns from c0 on (split: 64 of 128 for each tile's warps, the
+      // only 64 for A's): w0 O_A + w1 O_B when split (the
       // other tile's (m, l) come through shared memory), else w0 O_X
-      constexpr int W = SPLIT ? D / 2 : D;
-      const int c0 = SPLIT ? x * (D / 2) : 0;
+      const int c0 = SPLIT && D == 128 ? x * 64 : 0;
       float w0 = 1.f, w1 = 0.f;
       if constexpr (SPLIT) {
         float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + r;
@@ -775,37 +781,18 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       } else if (valid && (!SPLIT || x == 0)) {
         p.ws_ml[slot] = make_float2(m, l);
       }
-      T16* out = static_cast<T16*>(p.out) + row * D + c0;
-      float* wo = p.ws_o + slot * D + c0;
-      if (live) {
-#pragma unroll 1
-        for (int cc = 0; cc < W; cc += 32) {
-          uint32_t o[32], ob[SPLIT ? 32 : 1];
-          tc::ld32x32b_x32(tO + (SPLIT ? 0 : x * 128) + c0 + cc, o);
-          if constexpr (SPLIT) tc::ld32x32b_x32(tO + 128 + c0 + cc, ob);
-          tc::wait_ld();
-          if (valid) {
-            // a tile without weight may hold anything
-            float y[32];
+      if (live && !(SPLIT && D == 64 && x == 1)) {
+        const uint32_t ta = tO + (SPLIT ? 0 : x * 128) + c0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              y[e] = w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0;
-              if constexpr (SPLIT) y[e] += w1 == 0.f ? 0.f : __uint_as_float(ob[e]) * w1;
-            }
-            if (g.slot < 0) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(out + cc + e) =
-                    make_uint4(pack2<BF16>(y[e], y[e + 1]), pack2<BF16>(y[e + 2], y[e + 3]),
-                               pack2<BF16>(y[e + 4], y[e + 5]), pack2<BF16>(y[e + 6], y[e + 7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(wo + cc + e) =
-                    make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-            }
-          }
-          __syncwarp();
+        for (int cc = 0; cc < D; cc += 64) {
+          if (SPLIT && D == 128 && cc > 0) break;  // 64 of 128 columns each
+          if (g.slot < 0)
+            attn::store_rows<T16, SPLIT>(
+                ta + cc, ta + cc + 128,
+                valid ? static_cast<T16*>(p.out) + row * D + c0 + cc : nullptr, w0, w1);
+          else
+            attn::store_rows<float, SPLIT>(ta + cc, ta + cc + 128,
+                                           valid ? p.ws_o + slot * D + c0 + cc : nullptr, w0, w1);
         }
       }
       tc::fence_before();
@@ -828,10 +815,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
 
 // Combines the segments of the units split between shares.  CTA (c, y) looks
 // at the boundary between shares c and c + 1: if it cuts a unit whose first
-// step lies in share c, this CTA merges 32 of the unit's rows, a warp a row,
-// from the shares' slots in order.  Every other row was written whole.
+// step lies in share c, this CTA merges kMergeRows of the unit's rows, a warp a
+// row, from the shares' slots in order.  Every other row was written whole.
 template <typename OutT, int D, bool SPLIT>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int ctas) {
+__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeParams p, int ctas) {
   __shared__ int sh_s, sh_h, sh_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
@@ -840,13 +827,14 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int
   // the workspace is read
   if (warp == 0) {
     int s = -1, h = 0, last = c;
-    const Shares sh(total_weight(p, lane, false), ctas);
+    int first;
+    const Shares sh(total_weight(p, lane, false, first), ctas);
     if (c + 1 < sh.C) {
       const long long X = sh.start(c + 1);
       int s0, w;
       long long gs;
-      if (locate(p, X, lane, s0, gs, w)) {
-        h = (int)((X - gs) / w);
+      if (locate(p, X, lane, first, s0, gs, w)) {
+        h = quotient(X - gs, w);
         const long long u = gs + (long long)h * w + kSegCost, end = u + w - kSegCost;
         if (u < X && u >= sh.start(c)) {
           s = s0;
@@ -870,35 +858,40 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, int
   if (sh_s < 0) return;
   const int G = p.group, QT = kTileM / G, n = seq_nodes(p, sh_s), last = sh_last;
   constexpr int RW = SPLIT ? 128 : 256, V = D / 32;  // rows of a slot, floats a lane
-  for (int k = warp; k < 32; k += 8) {
-    const int row = blockIdx.y * 32 + k;  // of the CTAs side by side: RW each
-    const int rg = row / RW, in = row % RW, r = in % kTileM;
-    const int node = (row / kTileM) * QT + r / G;
-    if (r / G >= QT || node >= n) continue;
-    float M = -INFINITY, Ls = 0.f, acc[V] = {};
-#pragma unroll 4
-    for (int cc = c; cc <= last; ++cc) {
-      const size_t slot = ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
-      const float2 v = p.ws_ml[slot];
-      const float* o = p.ws_o + slot * D + lane * V;
-      float y[V];
+  const int row = blockIdx.y * kMergeRows + warp;    // of the CTAs side by side: RW each
+  const int rg = row / RW, in = row % RW, r = in % kTileM;
+  const int node = (row / kTileM) * QT + r / G;
+  if (r / G >= QT || node >= n) return;
+  auto slot = [&](int cc) -> size_t {
+    return ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
+  };
+  float M = -INFINITY, Ls = 0.f, acc[V] = {};
+  for (int c0 = c; c0 <= last; c0 += 32) {  // 32 pieces at a time, a lane each
+    const int k = min(32, last - c0 + 1);
+    const float2 v = lane < k ? p.ws_ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float mn = fmaxf(M, warp_max_xor(v.x, 1));
+    if (mn == -INFINITY) continue;
+    const float old = exp2f(M - mn), w = exp2f(v.x - mn);
+    M = mn;
+    Ls *= old;
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = o[e];
-      if (v.x == -INFINITY) continue;  // no key seen: y may hold anything
-      const float mn = fmaxf(M, v.x), wa = exp2f(M - mn), wb = exp2f(v.x - mn);
-      Ls = Ls * wa + v.y * wb;
+    for (int e = 0; e < V; ++e) acc[e] *= old;
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, v.y, i);
+      const float* o = p.ws_o + slot(c0 + i) * D + lane * V;
+      Ls += wi * li;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = acc[e] * wa + y[e] * wb;
-      M = mn;
+      for (int e = 0; e < V; ++e) acc[e] += wi == 0.f ? 0.f : wi * o[e];
     }
-    const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
-    constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
-    uint32_t* out = reinterpret_cast<uint32_t*>(
-        static_cast<OutT*>(p.out) +
-        (((size_t)sh_s * p.q_len + node) * p.n_q + sh_h * G + r % G) * D + lane * V);
-#pragma unroll
-    for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf>(acc[e] * inv, acc[e + 1] * inv);
   }
+  const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
+  constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
+  uint32_t* out = reinterpret_cast<uint32_t*>(
+      static_cast<OutT*>(p.out) +
+      (((size_t)sh_s * p.q_len + node) * p.n_q + sh_h * G + r % G) * D + lane * V);
+#pragma unroll
+  for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 template <bool BF16, int D, bool FP8, bool SPLIT>
@@ -916,8 +909,8 @@ cudaError_t launch_t(const TreeParams& p, const CUtensorMap* tmq, const CUtensor
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)shares, (SPLIT ? 128 : 256) / 32 * p.row_groups);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)shares, (SPLIT ? 128 : 256) / kMergeRows * p.row_groups);
+  cfg.blockDim = dim3(32 * kMergeRows);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
