@@ -43,7 +43,7 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11: see the roles
 constexpr int kItems = 4;              // items scheduled ahead
 constexpr uint32_t kItemReaders = 11;  // 8 softmax warps, MMA, loads, fixer
-constexpr uint32_t kTmemCols = 512;    // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 10;
 
 template <int D>
@@ -54,6 +54,20 @@ struct Lay {
   static constexpr int kBarOff = kKVOff + kStages * kOp;
   static constexpr int kSmem = kBarOff + 1024 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  // TMEM columns: S_A 0, S_B 128; a 64-wide head leaves room for P beside S, so
+  // that S of the next tile is made while the softmax works on this one
+  static constexpr bool kSepP = D == 64;
+  static constexpr int tP(int x) { return kSepP ? 256 + 64 * x : 128 * x; }
+  static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
+  // The o-th product of a step: true for S, false for O += P V, of tile x.  An
+  // item's first step ends the item before, whose last products do not wait
+  // for the new Q.  Where P lies over S, S of the next tile comes after O += P V
+  // (the tensor core keeps their order); else before it.
+  static __device__ __forceinline__ bool op_at(int j, int o, int& x) {
+    const bool pairs = j == 0 || kSepP;  // both of one kind, then both of the other
+    x = pairs ? o & 1 : o >> 1;
+    return pairs ? (o >> 1) == (j == 0 ? 1 : 0) : (o & 1) == 1;
+  }
   static_assert(kStages <= kMaxStages, "stage barriers");
 };
 
@@ -70,6 +84,7 @@ struct Bars {
   uint64_t raw[kMaxStages];  // a V tile whose tail warp 11 has yet to zero
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_empty[2], pv_done[2];  // P beside S only
   uint64_t done;
   Item items[kItems];
   uint32_t tmem_base;
@@ -144,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->s_full[x], 1);
       mbar_init(&B->p_half[x], 128);
       mbar_init(&B->p_full[x], 128);
+      mbar_init(&B->s_empty[x], 128);
+      mbar_init(&B->pv_done[x], 1);
       mbar_init(&B->o_full[x], 1);
       mbar_init(&B->o_free[x], 128);
     }
@@ -162,14 +179,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = B->tmem_base;
 
-  // 384 threads at 168 registers: 64,512 = 256 x 200 + 128 x 96 + 1,024 left
+  // 384 threads at 168 registers: 64,512 = 256 x 192 + 128 x 120
   if (warp >= kMmaWarp) {
-  tc::regs_dec<96>();
+  tc::regs_dec<120>();
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    // per key tile and X = A, B: O_X += P_X V of the tile before, then
-    // S_X = Q_X K^T over the P just read (the tensor core keeps their order).
-    // The whole warp walks the tiles and waits; one lane issues.
+    // per key tile j and X = A, B: O_X += P_X V of tile j - 1 and S_X = Q_X K^T
+    // of tile j, in the order of op_at.  The whole warp walks the tiles and
+    // waits; one lane issues.  One copy of each product's code: unrolled copies
+    // miss the instruction cache.
     constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
     constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
     const uint64_t dQ = tc::smem_desc(sbase + L::kQOff), dK = tc::smem_desc(sbase + L::kKVOff),
@@ -177,92 +195,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
     Reader rd;
     Item it;
-    bool ok = true, issued = false;
-    uint32_t c = 0;  // stages used before this tile
-    int n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
-    struct {
-      bool on = false, first, last, release;
-      int st;
-    } pend[2];
-    int vst = 0, q_items[2] = {0, 0};  // stage and parity of the tiles' V
-    uint32_t vpar = 0;
-    auto pv = [&](int x) -> bool {
-      auto& w = pend[x];
-      if (w.first && n_items[x] >= 2 && !wait_all(&B->o_free[x], (n_items[x] - 2) & 1, B, p.dev_err))
-        return false;
-      const uint64_t v = dV + w.st * kOpStep;
-      const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
-      const uint32_t par = (n_tiles[x] - 1) & 1;
-      // 16 keys a step = two 8-row groups of V
-      if (!wait_all(&B->p_half[x], par, B, p.dev_err)) return false;
-      tc::fence_after();
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (w.first && kk == 0) ? 0u : 1u);
-      }
+    bool ok = true, issued = false, more = true;
+    uint32_t c = 0;  // stages used before this tile: K of tile j in c, V in c + 1
+    int items0 = 0, items1 = 0, s0 = 0, s1 = 0, p0 = 0, p1 = 0, o0 = 0, o1 = 0;
+    int pj = -1, pn0 = 0, pn1 = 0;  // the tile before, and its item's tiles of A and B
+    while (ok && more) {
+      more = __all_sync(0xffffffffu, rd.next(B, p.dev_err, it));
+      if (more && lane == 0) rd.done(B);
       __syncwarp();
-      if (!wait_all(&B->p_full[x], par, B, p.dev_err)) return false;
-      tc::fence_after();
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int kk = 4; kk < 8; ++kk) tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
-        if (w.release) tc::commit(&B->empty[w.st]);
-        if (w.last) tc::commit(&B->o_full[x]);
-      }
-      __syncwarp();
-      w.on = false;
-      return true;
-    };
-    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
-      __syncwarp();
-      if (lane == 0) rd.done(B);
-      __syncwarp();
-      const int n = max(it.nkt[0], it.nkt[1]);
-      for (int j = 0; j < n && ok; ++j, c += 2) {
-        const int sk = c % NS, sv = (c + 1) % NS;
+      // after the last item one more step, for the products still to do
+      const int n0 = more ? it.nkt[0] : 0, n1 = more ? it.nkt[1] : 0, n = max(max(n0, n1), 1);
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t cv = c - 1;
+        const int sk = c % NS, sv = cv % NS;
         // what the next MMAs read besides P has usually landed long before P
         // is written: waited for first, off the chain P -> O += P V -> S
-        if (pend[0].on || pend[1].on) ok = wait_all(&B->full[vst], vpar, B, p.dev_err);
-        ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
-        vst = sv;
-        vpar = ((c + 1) / NS) & 1;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (ok && j == 0 && j < it.nkt[x])
-            ok = wait_all(&B->q_full[x], q_items[x]++ & 1, B, p.dev_err);
-          if (ok && pend[x].on) ok = pv(x);
-          if (!ok || j >= it.nkt[x]) continue;
-          n_items[x] += j == 0;
-          tc::fence_after();
-          const bool lastx = x == 1 || j >= it.nkt[1];  // the K tile's last reader of the two
-          const bool last = j == it.nkt[x] - 1;
-          if (tc::elect_one()) {
-            const uint64_t q = dQ + x * kOpStep, k = dK + sk * kOpStep;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-              tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
+        if (pj >= 0) ok = wait_all(&B->full[sv], (cv / NS) & 1, B, p.dev_err);
+        if (more && j > 0) ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+#pragma unroll 1
+        for (int o = 0; o < 4 && ok; ++o) {
+          int x;
+          if (L::op_at(j, o, x)) {
+            const int nx = x ? n1 : n0;
+            if (j >= nx) continue;
+            const int tiles = x ? s1 : s0;
+            if (j == 0) {
+              ok = wait_all(&B->q_full[x], (x ? items1 : items0) & 1, B, p.dev_err);
+              ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+              x ? ++items1 : ++items0;
             }
-            tc::commit(&B->s_full[x]);
-            if (lastx) tc::commit(&B->empty[sk]);
-            if (last) tc::commit(&B->q_empty[x]);
+            if (L::kSepP && tiles > 0)  // the softmax has read S of the tile before
+              ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+              const uint64_t q = dQ + x * kOpStep, k = dK + sk * kOpStep;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+                tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
+              }
+              tc::commit(&B->s_full[x]);
+              // the K tile's last reader of the two
+              if (x == 1 || j >= n1) tc::commit(&B->empty[sk]);
+              if (j == nx - 1) tc::commit(&B->q_empty[x]);
+            }
+            __syncwarp();
+            issued = true;
+            x ? ++s1 : ++s0;
+          } else {
+            const int nx = x ? pn1 : pn0;
+            if (pj < 0 || pj >= nx) continue;
+            const int before = x ? o1 : o0, par = (x ? p1 : p0) & 1;
+            if (pj == 0) {
+              if (before > 0) ok = wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
+              x ? ++o1 : ++o0;
+            }
+            const uint64_t v = dV + sv * kOpStep;
+            const uint32_t tP = tmem + L::tP(x), tO = tmem + L::tO(x);
+            // 16 keys a step = two 8-row groups of V
+            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (pj == 0 && kk == 0) ? 0u : 1u);
+            }
+            __syncwarp();
+            ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+              if (x == 1 || pj >= pn1) tc::commit(&B->empty[sv]);
+              if (L::kSepP) tc::commit(&B->pv_done[x]);
+              if (pj == nx - 1) tc::commit(&B->o_full[x]);
+            }
+            __syncwarp();
+            x ? ++p1 : ++p0;
           }
-          __syncwarp();
-          issued = true;
-          ++n_tiles[x];
-          pend[x].on = true;
-          pend[x].first = j == 0;
-          pend[x].last = last;
-          pend[x].release = lastx;
-          pend[x].st = sv;
         }
+        pj = j;
+        pn0 = n0;
+        pn1 = n1;
+        c += 2;
       }
     }
-    if (pend[0].on || pend[1].on) ok = ok && wait_all(&B->full[vst], vpar, B, p.dev_err);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (ok && pend[x].on) ok = pv(x);
     // everything issued above has completed before TMEM is released
     if (issued) {
       if (tc::elect_one()) tc::commit(&B->done);
@@ -419,11 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax
-    tc::regs_inc<200>();
+    tc::regs_inc<192>();
     const int x = warp >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row = TMEM lane
     const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tmem + x * 128 + lanes, tO = tmem + 256 + x * 128 + lanes;
+    const uint32_t tS = tmem + x * 128 + lanes, tP = tmem + L::tP(x) + lanes,
+                   tO = tmem + L::tO(x) + lanes;
     const float sl = p.scale_log2;
     Reader rd;
     Item it;
@@ -449,6 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = 0; w < 4; ++w) vis[w] = attn::bits_upto(j * kTileN + 32 * w, qi);
           float s[kTileN];
           attn::load_scores(tS, s);
+          if (L::kSepP) {
+            tc::fence_before();
+            mbar_arrive(&B->s_empty[x]);
+          }
           const float mx = attn::tile_max(s, full, vis, sl);
           const float mn = fmaxf(st.m, mx);
           const bool grow = mn > st.m + attn::kRescaleLog2;
@@ -458,21 +484,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             st.l *= alpha;
             st.m = mn;
           }
-          // S of this tile is done, so O += P V of the one before is too
-          if (j > 0 && __any_sync(0xffffffffu, grow)) attn::rescale_o(tO, D, alpha);
+          // O += P V of the tile before is done where P lies over S: S of this
+          // tile came after it
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            if (L::kSepP)
+              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+            tc::fence_after();
+            attn::rescale_o(tO, D, alpha);
+          }
           const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
           uint32_t pk[32];
           st.l += attn::tile_weights<BF16, 0>(s, 0, full, sl, neg_m, pk);
-          tc::st32x32b_x32(tS, pk);
+          if (L::kSepP && t > 0) {  // P of the tile before has been read
+            ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+            tc::fence_after();
+          }
+          tc::st32x32b_x32(tP, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
           st.l += attn::tile_weights<BF16, 0>(s, 1, full, sl, neg_m, pk);
-          tc::st32x32b_x32(tS + 32, pk);
+          tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_full[x]);
         } else {
+          if (L::kSepP) {
+            mbar_arrive(&B->s_empty[x]);
+            // not ahead of the other warps' P of the tile before
+            if (t > 0)
+              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+          }
           mbar_arrive(&B->p_half[x]);
           mbar_arrive(&B->p_full[x]);
         }

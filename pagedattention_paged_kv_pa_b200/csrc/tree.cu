@@ -52,7 +52,7 @@ using attn::kTileN;
 
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
 constexpr int kSegs = 4;  // segments scheduled ahead
-constexpr uint32_t kTmemCols = 512;  // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMergeRows = 16;  // rows of a merge CTA
 constexpr int kSegCost = 1;  // a unit's fixed costs, in steps
 
@@ -73,10 +73,25 @@ struct Lay {
   static constexpr int kBarOff = kRedOff + (SPLIT ? 2048 : 0);
   static constexpr int kSmem = kBarOff + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  // TMEM columns: S_A 0, S_B 128; a 64-wide head leaves room for P beside S, so
+  // that S of the next tile is made while the softmax works on this one
+  static constexpr bool kSepP = D == 64;
+  static constexpr int tP(int x) { return kSepP ? 256 + 64 * x : 128 * x; }
+  static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
+  // The o-th product of a step: true for S, false for O += P V, of tile x.  A
+  // segment's first step ends the one before, whose last products do not wait
+  // for the new Q (which, for E4M3, the softmax threads write after them).
+  // Where P lies over S, S of the next tile comes after O += P V (the tensor
+  // core keeps their order); else before it.
+  static __device__ __forceinline__ bool op_at(int j, int o, int& x) {
+    const bool pairs = j == 0 || kSepP;  // both of one kind, then both of the other
+    x = pairs ? o & 1 : o >> 1;
+    return pairs ? (o >> 1) == (j == 0 ? 1 : 0) : (o & 1) == 1;
+  }
   static constexpr int kThreads = FP8 ? 640 : 384;
   // registers: 640 x 96 = 61,440 = 256 x 128 + 384 x 72 + 1,024, or 384 x 168 =
-  // 64,512 = 256 x 200 + 128 x 96 + 1,024
-  static constexpr int kSoftRegs = FP8 ? 128 : 200, kOtherRegs = FP8 ? 72 : 96;
+  // 64,512 = 256 x 192 + 128 x 120
+  static constexpr int kSoftRegs = FP8 ? 128 : 192, kOtherRegs = FP8 ? 72 : 120;
   // readers of a segment: 8 softmax warps, MMA, K and V loads, 8 converters
   static constexpr uint32_t kReaders = FP8 ? 19 : 11;
 };
@@ -92,6 +107,7 @@ struct Bars {
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], raw_full[2][4], raw_empty[2][4];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], red[2];
+  uint64_t s_empty[2], pv_done[2];  // P beside S only
   uint64_t done;
   Seg segs[kSegs];
   uint32_t tmem_base;
@@ -319,6 +335,8 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       mbar_init(&B->s_full[x], 1);
       mbar_init(&B->p_half[x], 128);
       mbar_init(&B->p_full[x], 128);
+      mbar_init(&B->s_empty[x], 128);
+      mbar_init(&B->pv_done[x], 1);
       mbar_init(&B->o_full[x], 1);
       mbar_init(&B->o_free[x], SPLIT ? 256 : 128);
       mbar_init(&B->red[x], 128);
@@ -342,9 +360,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
     tc::regs_dec<L::kOtherRegs>();
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
-      // per step and X = A, B: O_X += P_X V of the step before, then
-      // S_X = Q_X K^T over the P just read.  The whole warp walks the steps
-      // and waits; one lane issues.
+      // per step j and X = A, B: O_X += P_X V of step j - 1 and S_X = Q_X K^T of
+      // step j, in the order of op_at.  The whole warp walks the steps and
+      // waits; one lane issues.  One copy of each product's code: unrolled
+      // copies miss the instruction cache.
       constexpr uint32_t idesc_s = tc::idesc_f16(kOpBf16, false, kTileM, kTileN);
       constexpr uint32_t idesc_pv = tc::idesc_f16(kOpBf16, true, kTileM, D);
       constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
@@ -352,98 +371,105 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
                      dV = tc::smem_desc(sbase + L::kVOff, 16384);
       Reader rd;
       Seg g;
-      bool ok = true, issued = false;
-      uint32_t c = 0;  // key tiles before this segment
-      int n_segs = 0, n_items[2] = {0, 0}, n_tiles[2] = {0, 0};
-      struct {
-        bool on = false, first, last, release;
-        uint32_t tile;  // its V tile, counted over all segments
-        int before;     // O buffers of X read out before this one (for `first`)
-      } pend[2];
-      auto pv = [&](int x) -> bool {
-        auto& w = pend[x];
-        if (w.first && w.before > 0 &&
-            !wait_all(&B->o_free[x], (w.before - 1) & 1, B, p.dev_err))
-          return false;
-        const int st = w.tile % VS;
-        if (!wait_all(&B->v_full[st], (w.tile / VS) & 1, B, p.dev_err)) return false;
-        const uint64_t v = dV + st * kOpStep;
-        const uint32_t tP = tmem + x * 128, tO = tmem + 256 + x * 128;
-        const uint32_t par = (n_tiles[x] - 1) & 1;
-        if (!wait_all(&B->p_half[x], par, B, p.dev_err)) return false;
-        tc::fence_after();
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
-            tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (w.first && kk == 0) ? 0u : 1u);
-        }
+      bool ok = true, issued = false, more = true;
+      uint32_t c = 0, pc = 0;  // key tiles before this segment, and before the last one
+      int segs = 0, items0 = 0, items1 = 0, s0 = 0, s1 = 0, p0 = 0, p1 = 0, o0 = 0, o1 = 0;
+      int pj = -1, pn0 = 0, pn1 = 0;  // the step before, and its segment's steps of A and B
+      while (ok && more) {
+        more = __all_sync(0xffffffffu, rd.next(B, p.dev_err, g));
+        if (more && lane == 0) rd.done(B);
         __syncwarp();
-        if (!wait_all(&B->p_full[x], par, B, p.dev_err)) return false;
-        tc::fence_after();
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk) tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
-          if (w.release) tc::commit(&B->v_empty[st]);
-          if (w.last) tc::commit(&B->o_full[x]);
-        }
-        __syncwarp();
-        w.on = false;
-        return true;
-      };
-      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
-        __syncwarp();
-        if (lane == 0) rd.done(B);
-        const int nt = g.t1 - g.t0, steps = SPLIT ? (nt + 1) / 2 : nt;
-        const bool live1 = SPLIT ? nt > 1 : tile_nodes(g, 1) > 0;  // A always has a tile
-        if (SPLIT) {
-          // E4M3: the query rows come from the softmax threads, after the
-          // segment before, whose last products they wait for
-          if (FP8 && pend[0].on) ok = pv(0);
-          if (FP8 && ok && pend[1].on) ok = pv(1);
-          ok = ok && wait_all(&B->q_full[0], n_segs & 1, B, p.dev_err);
-        }
-        for (int j = 0; j < steps && ok; ++j) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (ok && pend[x].on) ok = pv(x);
-            const int ti = SPLIT ? 2 * j + x : j;
-            if (!ok || ti >= nt || (x == 1 && !live1)) continue;
-            if (!SPLIT && j == 0) ok = wait_all(&B->q_full[x], n_items[x] & 1, B, p.dev_err);
-            const uint32_t tile = c + ti;
-            const int sk = tile % KS;
-            ok = ok && wait_all(&B->k_full[sk], (tile / KS) & 1, B, p.dev_err);
-            if (!ok) continue;
-            tc::fence_after();
-            const bool lastx = SPLIT || x == 1 || !live1;  // the K/V tile's last reader
-            const bool last = SPLIT ? ti + 2 >= nt : j == nt - 1;
-            if (tc::elect_one()) {
-              const uint64_t q = dQ + (SPLIT ? 0 : x) * kOpStep, k = dK + sk * kOpStep;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-                tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
+        const int nt = more ? g.t1 - g.t0 : 0;
+        const int n0 = SPLIT ? (nt + 1) / 2 : nt;  // A always has a tile
+        const int n1 = SPLIT ? nt / 2 : (more && tile_nodes(g, 1) > 0 ? nt : 0);
+        // after the last segment one more step, for the products still to do
+        const int n = max(n0, 1);
+        for (int j = 0; j < n && ok; ++j) {
+#pragma unroll 1
+          for (int o = 0; o < 4 && ok; ++o) {
+            int x;
+            if (L::op_at(j, o, x)) {
+              const int nx = x ? n1 : n0;
+              if (j >= nx) continue;
+              const int tiles = x ? s1 : s0;
+              if (j == 0) {
+                if (x == 0 || !SPLIT)
+                  ok = wait_all(&B->q_full[x], (SPLIT ? segs : (x ? items1 : items0)) & 1, B,
+                                p.dev_err);
+                x ? ++items1 : ++items0;
               }
-              tc::commit(&B->s_full[x]);
-              if (lastx) tc::commit(&B->k_empty[sk]);
-              if (SPLIT ? ti == nt - 1 : last) tc::commit(&B->q_empty[SPLIT ? 0 : x]);
+              const uint32_t tile = c + (SPLIT ? 2 * j + x : j);
+              const int sk = tile % KS;
+              ok = ok && wait_all(&B->k_full[sk], (tile / KS) & 1, B, p.dev_err);
+              if (L::kSepP && tiles > 0)  // the softmax has read S of the tile before
+                ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+              if (!ok) break;
+              tc::fence_after();
+              if (tc::elect_one()) {
+                const uint64_t q = dQ + (SPLIT ? 0 : x) * kOpStep, k = dK + sk * kOpStep;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+                  tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
+                }
+                tc::commit(&B->s_full[x]);
+                // the K tile's last reader of the two
+                if (SPLIT || x == 1 || n1 == 0) tc::commit(&B->k_empty[sk]);
+                if (SPLIT ? 2 * j + x == nt - 1 : j == nx - 1)
+                  tc::commit(&B->q_empty[SPLIT ? 0 : x]);
+              }
+              __syncwarp();
+              issued = true;
+              x ? ++s1 : ++s0;
+            } else {
+              const int nx = x ? pn1 : pn0;
+              if (pj < 0 || pj >= nx) continue;
+              const uint32_t tile = pc + (SPLIT ? 2 * pj + x : pj);
+              const int sv = tile % VS, par = (x ? p1 : p0) & 1;
+              ok = wait_all(&B->v_full[sv], (tile / VS) & 1, B, p.dev_err);
+              if (pj == 0) {
+                // O_X has been read out as often as there were segments before
+                // (split), or segments with a tile of X
+                const int before = SPLIT ? segs - (j == 0 ? 1 : 0) : (x ? o1 : o0);
+                if (before > 0)
+                  ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
+                x ? ++o1 : ++o0;
+              }
+              const uint64_t v = dV + sv * kOpStep;
+              const uint32_t tP = tmem + L::tP(x), tO = tmem + L::tO(x);
+              ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+              if (!ok) break;
+              tc::fence_after();
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
+                  tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv,
+                             (pj == 0 && kk == 0) ? 0u : 1u);
+              }
+              __syncwarp();
+              ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+              if (!ok) break;
+              tc::fence_after();
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk)
+                  tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+                if (SPLIT || x == 1 || pn1 == 0) tc::commit(&B->v_empty[sv]);
+                if (L::kSepP) tc::commit(&B->pv_done[x]);
+                if (pj == nx - 1) tc::commit(&B->o_full[x]);
+              }
+              __syncwarp();
+              x ? ++p1 : ++p0;
             }
-            __syncwarp();
-            issued = true;
-            ++n_tiles[x];
-            pend[x].on = true;
-            pend[x].first = j == 0;
-            pend[x].last = last;
-            pend[x].release = lastx;
-            pend[x].tile = tile;
-            if (j == 0) pend[x].before = SPLIT ? n_segs : n_items[x]++;
           }
+          pj = j;
+          pn0 = n0;
+          pn1 = n1;
+          pc = c;
         }
         c += nt;
-        ++n_segs;
+        ++segs;
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (ok && pend[x].on) ok = pv(x);
       // everything issued above has completed before TMEM is released
       if (issued) {
         if (tc::elect_one()) tc::commit(&B->done);
@@ -626,7 +652,8 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
     const int r = q4 * 32 + lane;  // row = TMEM lane
     const int ri = r / G, rh = r - ri * G;  // its node within the tile, its head
     const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tmem + x * 128 + lanes, tO = tmem + 256 + lanes;
+    const uint32_t tS = tmem + x * 128 + lanes, tP = tmem + L::tP(x) + lanes,
+                   tO = tmem + L::tO(x) + lanes;
     // rows without a node, and sequences without context: zeros
     if (rg == 0)
       for (int s = blockIdx.x / nrg; s < p.num_seqs; s += gridDim.x / nrg) {
@@ -706,6 +733,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             mx = attn::tile_max_halves(tS, full, vis, sl);
           } else {
             attn::load_scores(tS, s);
+            if (L::kSepP) {
+              tc::fence_before();
+              mbar_arrive(&B->s_empty[x]);
+            }
             mx = attn::tile_max(s, full, vis, sl);
           }
           const float mn = fmaxf(m, mx);
@@ -716,24 +747,47 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             l *= alpha;
             m = mn;
           }
-          // S of this tile is done, so O += P V of the one before is too
-          if (any && __any_sync(0xffffffffu, grow)) attn::rescale_o(tO + x * 128, D, alpha);
+          // O += P V of the tile before is done where P lies over S: S of this
+          // tile came after it
+          if (any && __any_sync(0xffffffffu, grow)) {
+            if (L::kSepP)
+              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+            tc::fence_after();
+            attn::rescale_o(tO, D, alpha);
+          }
           // a row that has seen no key yet: its weights are 0
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
           if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
           l += attn::tile_weights<kOpBf16, 0>(s, 0, full, sl, neg_m, pk);
-          tc::st32x32b_x32(tS, pk);
+          if (L::kSepP && t > 0) {  // P of the tile before has been read
+            ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+            tc::fence_after();
+          }
+          tc::st32x32b_x32(tP, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
           if constexpr (FP8) attn::load_half(tS, 1, full, vis, sl, s);
+          if (FP8 && L::kSepP) {
+            tc::fence_before();
+            mbar_arrive(&B->s_empty[x]);
+          }
           l += attn::tile_weights<kOpBf16, 0>(s, FP8 ? 0 : 1, full, sl, neg_m, pk);
-          tc::st32x32b_x32(tS + 32, pk);
+          tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_full[x]);
         } else {
+          if (L::kSepP) {
+            mbar_arrive(&B->s_empty[x]);
+            // not ahead of the other warps' P of the tile before
+            if (t > 0)
+              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            if (!ok) break;
+          }
           mbar_arrive(&B->p_half[x]);
           mbar_arrive(&B->p_full[x]);
         }
@@ -782,16 +836,17 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         p.ws_ml[slot] = make_float2(m, l);
       }
       if (live && !(SPLIT && D == 64 && x == 1)) {
-        const uint32_t ta = tO + (SPLIT ? 0 : x * 128) + c0;
+        const uint32_t ta = tmem + L::tO(SPLIT ? 0 : x) + lanes + c0,
+                       tb = tmem + L::tO(1) + lanes + c0;
 #pragma unroll
         for (int cc = 0; cc < D; cc += 64) {
           if (SPLIT && D == 128 && cc > 0) break;  // 64 of 128 columns each
           if (g.slot < 0)
             attn::store_rows<T16, SPLIT>(
-                ta + cc, ta + cc + 128,
+                ta + cc, tb + cc,
                 valid ? static_cast<T16*>(p.out) + row * D + c0 + cc : nullptr, w0, w1);
           else
-            attn::store_rows<float, SPLIT>(ta + cc, ta + cc + 128,
+            attn::store_rows<float, SPLIT>(ta + cc, tb + cc,
                                            valid ? p.ws_o + slot * D + c0 + cc : nullptr, w0, w1);
         }
       }
