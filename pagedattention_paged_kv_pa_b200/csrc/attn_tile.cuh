@@ -86,23 +86,20 @@ __device__ __forceinline__ void load_scores(uint32_t ts, float (&x)[kTileN]) {
 }
 
 // Largest score of the row in log2 units; with a mask (full false) x becomes
-// the scores in log2 units, -inf where vis has no bit.
+// the scores in log2 units, -inf where vis has no bit, and sl 1.
 __device__ __forceinline__ float tile_max(float (&x)[kTileN], bool full, const uint32_t (&vis)[4],
-                                          float sl) {
+                                          float& sl) {
+  if (!full) {
+#pragma unroll
+    for (int e = 0; e < kTileN; ++e) x[e] = (vis[e >> 5] >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
+    sl = 1.f;
+  }
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  if (full) {
 #pragma unroll
-    for (int e = 0; e < kTileN; e += 8)
+  for (int e = 0; e < kTileN; e += 8)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(x[e + 2 * c], x[e + 2 * c + 1]));
-    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
-  }
-#pragma unroll
-  for (int e = 0; e < kTileN; ++e) {
-    x[e] = (vis[e >> 5] >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
-    m4[e & 3] = fmaxf(m4[e & 3], x[e]);
-  }
-  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], fmaxf(x[e + 2 * c], x[e + 2 * c + 1]));
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
 }
 
 // The same 64 keys at a time, for kernels whose threads cannot hold 128 scores:
@@ -150,35 +147,27 @@ __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
   tc::wait_st();
 }
 
-// Weights of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns their
-// fp32 sum.  Of every 8 pairs without a mask kPoly go through exp2_poly2.
+// Weights 2^(x sl - m) of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns
+// their fp32 sum.  Masked scores are -inf, with sl = 1 (tile_max has scaled the
+// others), so that tiles with and without a mask run the same code.  Of every
+// 8 pairs kPoly go through exp2_poly2 (which must not see a masked score).
 template <bool BF16, int kPoly>
-__device__ __forceinline__ float tile_weights(const float* x, int h, bool full, float sl,
-                                              float neg_m, uint32_t (&pk)[32]) {
+__device__ __forceinline__ float tile_weights(const float* x, int h, float sl, float neg_m,
+                                              uint32_t (&pk)[32]) {
   uint64_t s[2] = {0ull, 0ull};
   const uint64_t nm = f2(neg_m, neg_m), s2 = f2(sl, sl);
-  if (full) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      float a, b;
-      un2(fma2(f2(x[64 * h + 2 * c], x[64 * h + 2 * c + 1]), s2, nm), a, b);
-      if ((c & 7) < kPoly) {
-        exp2_poly2(a, b);
-      } else {
-        a = tc::ex2(a);
-        b = tc::ex2(b);
-      }
-      s[c & 1] = add2(s[c & 1], f2(a, b));
-      pk[c] = pack2<BF16>(a, b);
+  for (int c = 0; c < 32; ++c) {
+    float a, b;
+    un2(fma2(f2(x[64 * h + 2 * c], x[64 * h + 2 * c + 1]), s2, nm), a, b);
+    if ((c & 7) < kPoly) {
+      exp2_poly2(a, b);
+    } else {
+      a = tc::ex2(a);
+      b = tc::ex2(b);
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float a = tc::ex2(x[64 * h + 2 * c] + neg_m);
-      const float b = tc::ex2(x[64 * h + 2 * c + 1] + neg_m);
-      s[c & 1] = add2(s[c & 1], f2(a, b));
-      pk[c] = pack2<BF16>(a, b);
-    }
+    s[c & 1] = add2(s[c & 1], f2(a, b));
+    pk[c] = pack2<BF16>(a, b);
   }
   float a, b;
   un2(add2(s[0], s[1]), a, b);

@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before();
             mbar_arrive(&B->s_empty[x]);
           }
-          const float mx = attn::tile_max(s, full, vis, sl);
+          float sle = sl;
+          const float mx = attn::tile_max(s, full, vis, sle);
           const float mn = fmaxf(st.m, mx);
           const bool grow = mn > st.m + attn::kRescaleLog2;
           float alpha = 1.f;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
           uint32_t pk[32];
-          st.l += attn::tile_weights<BF16, 0>(s, 0, full, sl, neg_m, pk);
+          st.l += attn::tile_weights<BF16, 0>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
             ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
             if (!ok) break;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
-          st.l += attn::tile_weights<BF16, 0>(s, 1, full, sl, neg_m, pk);
+          st.l += attn::tile_weights<BF16, 0>(s, 1, sle, neg_m, pk);
           tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();

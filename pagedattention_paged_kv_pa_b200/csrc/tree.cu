@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] = seen_bits(key + 32 * w, P, mask);
           float s[FP8 ? 64 : kTileN];
-          float mx;
+          float mx, sle = FP8 && !full ? 1.f : sl;
           if constexpr (FP8) {
             mx = attn::tile_max_halves(tS, full, vis, sl);
           } else {
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
               tc::fence_before();
               mbar_arrive(&B->s_empty[x]);
             }
-            mx = attn::tile_max(s, full, vis, sl);
+            mx = attn::tile_max(s, full, vis, sle);
           }
           const float mn = fmaxf(m, mx);
           const bool grow = mn > m + attn::kRescaleLog2;
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
           if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
-          l += attn::tile_weights<kOpBf16, 0>(s, 0, full, sl, neg_m, pk);
+          l += attn::tile_weights<kOpBf16, 0>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
             ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
             if (!ok) break;
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             tc::fence_before();
             mbar_arrive(&B->s_empty[x]);
           }
-          l += attn::tile_weights<kOpBf16, 0>(s, FP8 ? 0 : 1, full, sl, neg_m, pk);
+          l += attn::tile_weights<kOpBf16, 0>(s, FP8 ? 0 : 1, sle, neg_m, pk);
           tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();
