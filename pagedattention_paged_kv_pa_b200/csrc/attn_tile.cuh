@@ -26,6 +26,40 @@ constexpr int kTileM = 128;           // rows of a tile: one per TMEM lane
 constexpr int kTileN = 128;           // keys per tile
 constexpr float kRescaleLog2 = 8.f;   // lazy rescale threshold (factor 256)
 
+// ------------------------------------------------------------------- waits
+// A bounded wait in few instructions (the kernels have dozens of them, and
+// their code would otherwise outgrow the instruction caches): it gives up after
+// a second, or when another role of the CTA has given up.  Giving up flags
+// PA_DEVERR_TIMEOUT.
+constexpr uint32_t kWaitNs = 1000000000u;  // below 2^31: the timer's low word wraps
+
+__device__ __forceinline__ uint32_t timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+template <typename Bars>
+__device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
+                                        int32_t* dev_err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = timer_lo();
+#pragma unroll 1
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&B->abort_flag)) return false;
+  } while (timer_lo() - t0 < kWaitNs);
+  flag_error(dev_err, PA_DEVERR_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
+  return false;
+}
+// the same for a whole warp, which goes on or gives up together
+template <typename Bars>
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
+                                         int32_t* dev_err) {
+  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
+}
+
 // ------------------------------------------------- two fp32 values at a time
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -207,7 +241,7 @@ __device__ __forceinline__ void store_rows(uint32_t ta, uint32_t tb, OutT* row, 
   constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
   const int lane = threadIdx.x & 31, q = lane & 3;
   const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
-#pragma unroll
+#pragma unroll 1
   for (int hf = 0; hf < 2; ++hf) {  // rows 0 .. 15, then 16 .. 31
     uint32_t a[32], b[TWO ? 32 : 1];
     tc::ld16x256b_x8(ta + ((uint32_t)(16 * hf) << 16), a);

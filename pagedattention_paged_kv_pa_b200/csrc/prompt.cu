@@ -92,20 +92,8 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
-__device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
-                                        int32_t* dev_err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (mbar_wait(bar, parity)) return *reinterpret_cast<volatile int*>(&B->abort_flag) == 0;
-  flag_error(dev_err, PA_DEVERR_TIMEOUT);
-  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
-  return false;
-}
-
-// the same for a whole warp, which goes on or gives up together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
-                                         int32_t* dev_err) {
-  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
-}
+using attn::wait_all;
+using attn::wait_ok;
 
 // The item stream as one role reads it.
 struct Reader {
@@ -345,30 +333,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     // level = position of an item in its sequence, in items; the levels are
     // walked downwards, within a level the sequences that reach it in order,
     // and the head groups of each
-    const int hgroups = p.n_q >> lhb, span = 2 * QT;
+    const unsigned hgroups = p.n_q >> lhb;
+    const int lspan = 8 - lhb, span = 1 << lspan;  // queries of an item
     auto items_of = [&](int s) -> int {
       int start;
       bool bad;
-      return s < p.num_seqs ? (seq_span(p, s, start, bad) + span - 1) / span : 0;
+      return s < p.num_seqs ? (seq_span(p, s, start, bad) + span - 1) >> lspan : 0;
     };
     int top = 0;
+#pragma unroll 1
     for (int s = lane; s < p.num_seqs; s += 32) {
       int start;
       bool bad;
-      top = max(top, (seq_span(p, s, start, bad) + span - 1) / span);
+      top = max(top, (seq_span(p, s, start, bad) + span - 1) >> lspan);
       if (bad && blockIdx.x == 0) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
     }
     for (int m = 16; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
     const int first = items_of(lane);  // of the first 32 sequences, kept
     int level = top, cnt = 0;
-    long long base = 0;  // (sequence, level) pairs before this level
+    unsigned base = 0;  // (sequence, level) pairs before this level
     bool more = true;
     for (int k = 0; more; ++k) {
       // there and back: the CTA that got the longest item of one round gets
       // the shortest of the next
-      const long long idx = (long long)k * gridDim.x +
-                            ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const long long want = idx / hgroups;
+      const unsigned idx =
+          (unsigned)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const unsigned want = idx / hgroups;
       while (more && want >= base + cnt) {
         base += cnt;
         --level;
@@ -377,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           more = false;
         } else {
           int n = first > level;
+#pragma unroll 1
           for (int s = 32 + lane; s < p.num_seqs; s += 32) n += items_of(s) > level;
           cnt = __reduce_add_sync(0xffffffffu, n);
         }
@@ -385,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.start = -1;
       if (more) {
         int r = (int)(want - base), seq = -1;
+#pragma unroll 1
         for (int s0 = 0; seq < 0 && s0 < p.num_seqs; s0 += 32) {
           const bool has = (s0 == 0 ? first : items_of(s0 + lane)) > level;
           const uint32_t m = __ballot_sync(0xffffffffu, has);
@@ -396,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool bad;
         it.len = seq_span(p, max(seq, 0), it.start, bad);
         it.i0 = level * span;
-        it.h0 = (int)(idx % hgroups) << lhb;
+        it.h0 = (int)(idx - want * hgroups) << lhb;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int i = it.i0 + x * QT;
@@ -425,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int valid = it.len - (n - 1) * kTileN;  // rows of the last tile
       if (valid >= kTileN) continue;
       const int st = (c - 1) % NS;
-      if (!__all_sync(0xffffffffu, wait_ok(&B->raw[st], (phase >> st) & 1, B, p.dev_err))) break;
+      if (!wait_all(&B->raw[st], (phase >> st) & 1, B, p.dev_err)) break;
       phase ^= 1u << st;
       uint8_t* d = smem + L::kKVOff + st * L::kOp;
       // 128-byte rows; the swizzle stays within a row
@@ -461,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = qw < it.len;
       attn::RowState st{-INFINITY, 0.f};
       for (int j = 0; j < nkt; ++j, ++t) {
-        ok = __all_sync(0xffffffffu, wait_ok(&B->s_full[x], t & 1, B, p.dev_err));
+        ok = wait_all(&B->s_full[x], t & 1, B, p.dev_err);
         if (!ok) break;
         if (live) {  // rows behind the sequence: nothing reads their P or O
           tc::fence_after();
@@ -489,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // tile came after it
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             if (L::kSepP)
-              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
             tc::fence_after();
             attn::rescale_o(tO, D, alpha);
@@ -498,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[32];
           st.l += attn::tile_weights<BF16, 0>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
-            ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
             tc::fence_after();
           }
@@ -516,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&B->s_empty[x]);
             // not ahead of the other warps' P of the tile before
             if (t > 0)
-              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
           }
           mbar_arrive(&B->p_half[x]);
@@ -524,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, wait_ok(&B->o_full[x], n_mine & 1, B, p.dev_err));
+      ok = wait_all(&B->o_full[x], n_mine & 1, B, p.dev_err);
       if (!ok) break;
       ++n_mine;
       const bool valid = qi < it.len;
@@ -534,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!valid) out = nullptr;
       tc::fence_after();
       if (live) {
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D; cc += 64)
           attn::store_rows<T16, false>(tO + cc, 0, out ? out + cc : nullptr, inv, 0.f);
         tc::fence_before();

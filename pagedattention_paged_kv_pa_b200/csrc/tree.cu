@@ -115,20 +115,8 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
 
-__device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
-                                        int32_t* dev_err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (mbar_wait(bar, parity)) return *reinterpret_cast<volatile int*>(&B->abort_flag) == 0;
-  flag_error(dev_err, PA_DEVERR_TIMEOUT);
-  *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
-  return false;
-}
-
-// the same for a whole warp, which goes on or gives up together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
-                                         int32_t* dev_err) {
-  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
-}
+using attn::wait_all;
+using attn::wait_ok;
 
 // The segment stream as one role reads it.
 struct Reader {
@@ -152,7 +140,7 @@ __device__ __forceinline__ int seq_nodes(const TreeParams& p, int s) {
 }
 __device__ __forceinline__ int seq_steps(const TreeParams& p, int s) {
   const int n = seq_nodes(p, s), c = seq_ctx(p, s);
-  return n > 0 ? (c + p.step_keys - 1) / p.step_keys : 0;
+  return n > 0 ? (c + p.step_keys - 1) >> p.log2_step : 0;
 }
 __device__ __forceinline__ int weight(int steps) { return steps > 0 ? steps + kSegCost : 0; }
 
@@ -160,9 +148,11 @@ __device__ __forceinline__ int weight(int steps) { return steps > 0 ? steps + kS
 // of range when `report`
 __device__ long long total_weight(const TreeParams& p, int lane, bool report, int& first) {
   long long part = first = lane < p.num_seqs ? weight(seq_steps(p, lane)) : 0;
+#pragma unroll 1
   for (int s = 32 + lane; s < p.num_seqs; s += 32) part += weight(seq_steps(p, s));
   if (report) {
     int err = 0;
+#pragma unroll 1
     for (int s = lane; s < p.num_seqs; s += 32) {
       const int n = p.tree_lens ? __ldg(&p.tree_lens[s]) : p.q_len;
       if (n < 0 || n > p.q_len) err |= PA_DEVERR_QUERY_LOC;
@@ -193,6 +183,7 @@ struct Shares {
 __device__ bool locate(const TreeParams& p, long long X, int lane, int first, int& s_out,
                        long long& gs_out, int& w_out) {
   long long acc = 0;
+#pragma unroll 1
   for (int base = 0; base < p.num_seqs; base += 32) {
     const int s = base + lane;
     const int n = base == 0 ? first : (s < p.num_seqs ? weight(seq_steps(p, s)) : 0);
@@ -660,6 +651,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         const int from = seq_ctx(p, s) > 0 ? seq_nodes(p, s) : 0;
         uint4* o = reinterpret_cast<uint4*>(static_cast<T16*>(p.out) +
                                             (size_t)s * p.q_len * p.n_q * D);
+#pragma unroll 1
         for (int i = from * p.n_q * D / 8 + threadIdx.x; i < p.q_len * p.n_q * D / 8; i += 256)
           o[i] = make_uint4(0, 0, 0, 0);
       }
@@ -703,7 +695,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         }
         if (!SPLIT || x == 0) {
           if (seg > 0)
-            ok = __all_sync(0xffffffffu, wait_ok(&B->q_empty[x], (seg - 1) & 1, B, p.dev_err));
+            ok = wait_all(&B->q_empty[x], (seg - 1) & 1, B, p.dev_err);
           if (!ok) break;
           uint8_t* d = smem + L::kQOff + x * L::kOp;
 #pragma unroll
@@ -718,7 +710,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       const int nt = g.t1 - g.t0;
       bool any = false;
       for (int ti = SPLIT ? x : 0; ti < nt; ti += SPLIT ? 2 : 1, ++t) {
-        ok = __all_sync(0xffffffffu, wait_ok(&B->s_full[x], t & 1, B, p.dev_err));
+        ok = wait_all(&B->s_full[x], t & 1, B, p.dev_err);
         if (!ok) break;
         if (live) {  // rows without a node: nothing reads their P or O
           tc::fence_after();
@@ -751,7 +743,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           // tile came after it
           if (any && __any_sync(0xffffffffu, grow)) {
             if (L::kSepP)
-              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
             tc::fence_after();
             attn::rescale_o(tO, D, alpha);
@@ -762,7 +754,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
           l += attn::tile_weights<kOpBf16, 0>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
-            ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+            ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
             tc::fence_after();
           }
@@ -785,7 +777,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             mbar_arrive(&B->s_empty[x]);
             // not ahead of the other warps' P of the tile before
             if (t > 0)
-              ok = __all_sync(0xffffffffu, wait_ok(&B->pv_done[x], (t - 1) & 1, B, p.dev_err));
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
           }
           mbar_arrive(&B->p_half[x]);
@@ -796,7 +788,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       if (!ok) break;
       // ------------------------------------------------ segment epilogue
       if (any) {
-        ok = __all_sync(0xffffffffu, wait_ok(&B->o_full[x], n_mine & 1, B, p.dev_err));
+        ok = wait_all(&B->o_full[x], n_mine & 1, B, p.dev_err);
         if (!ok) break;
         ++n_mine;
       }
@@ -809,12 +801,12 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + r;
         // (the segment before was read out by both)
         if (seg > 0)
-          ok = __all_sync(0xffffffffu, wait_ok(&B->o_free[0], (seg - 1) & 1, B, p.dev_err));
+          ok = wait_all(&B->o_free[0], (seg - 1) & 1, B, p.dev_err);
         if (!ok) break;
         red[x * 128] = make_float2(m, l);
         tc::fence_before();
         mbar_arrive(&B->red[x]);
-        ok = __all_sync(0xffffffffu, wait_ok(&B->red[x ^ 1], seg & 1, B, p.dev_err));
+        ok = wait_all(&B->red[x ^ 1], seg & 1, B, p.dev_err);
         if (!ok) break;
         const float2 a = red[0], b = red[128];
         m = fmaxf(a.x, b.x);
@@ -838,7 +830,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       if (live && !(SPLIT && D == 64 && x == 1)) {
         const uint32_t ta = tmem + L::tO(SPLIT ? 0 : x) + lanes + c0,
                        tb = tmem + L::tO(1) + lanes + c0;
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D; cc += 64) {
           if (SPLIT && D == 128 && cc > 0) break;  // 64 of 128 columns each
           if (g.slot < 0)
@@ -894,6 +886,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
         if (u < X && u >= sh.start(c)) {
           s = s0;
           // the last share with steps of the unit
+#pragma unroll 1
           for (int k = c + 1 + lane;; k += 32) {
             const uint32_t in = __ballot_sync(0xffffffffu, k < sh.C && sh.start(k) < end);
             last += __popc(in);
@@ -921,6 +914,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
     return ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
   };
   float M = -INFINITY, Ls = 0.f, acc[V] = {};
+#pragma unroll 1
   for (int c0 = c; c0 <= last; c0 += 32) {  // 32 pieces at a time, a lane each
     const int k = min(32, last - c0 + 1);
     const float2 v = lane < k ? p.ws_ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.f);
@@ -931,7 +925,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
     Ls *= old;
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] *= old;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < k; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, v.y, i);
       const float* o = p.ws_o + slot(c0 + i) * D + lane * V;
@@ -1001,6 +995,7 @@ cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspa
   const int qt = kTileM / p.group, tiles = (p.q_len + qt - 1) / qt;
   p.row_groups = tiles > 2 ? 2 : 1;
   p.step_keys = tiles == 1 ? 2 * kTileN : kTileN;
+  p.log2_step = tiles == 1 ? 8 : 7;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (size_t)kTreeCtas * 2 * (tiles == 1 ? 128 : 256) * D);
   if (D == 128)
