@@ -150,27 +150,38 @@ def _check(status: int, what: str):
 
 
 def _on_device(ref, *ts):
-    """Every tensor of a call lives on `ref`'s CUDA device."""
+    """The index of `ref`'s CUDA device; every tensor of a call lives on it."""
+    dev = ref.get_device()  # -1: not a CUDA tensor
     for t in ts:
-        if t is not None and t.device != ref.device:
+        if t is not None and t.get_device() != dev:
             raise PAError(PA_ERR_INVALID_ARG, f"a tensor is on {t.device}, not {ref.device}")
-    if ref.device.type != "cuda":
+    if dev < 0:
         raise PAError(PA_ERR_INVALID_ARG, "tensors must be on a CUDA device")
+    return dev
 
 
-class _current:
-    """Makes `device` the current one for a launch (its stream's device)."""
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, device):
-        self._to, self._was = device.index, torch.cuda.current_device()
 
-    def __enter__(self):
-        if self._to != self._was:
-            torch.cuda.set_device(self._to)
-
-    def __exit__(self, *exc):
-        if self._to != self._was:
-            torch.cuda.set_device(self._was)
+def _launch(dev: int, stream, what: str, fn, *args):
+    """Calls fn(*args, stream) with `dev` as the current device; stream None:
+    the device's current stream."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    was = torch.cuda.current_device()
+    if was == dev:
+        st = fn(*args, raw)
+    else:
+        torch.cuda.set_device(dev)
+        try:
+            st = fn(*args, raw)
+        finally:
+            torch.cuda.set_device(was)
+    if st != PA_OK:
+        raise PAError(st, what)
 
 
 def _contig(*ts):
@@ -272,14 +283,15 @@ def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, sc
     attends to the context before the tree and to the nodes j whose bit is set
     in masks[s, i] (int64, see tree_masks)."""
     _contig(out, q, k_pool, v_pool, block_tables, context_lens, masks, tree_lens, workspace)
-    _on_device(q, out, k_pool, v_pool, block_tables, context_lens, masks, tree_lens, workspace,
-               dev_err)
-    num_seqs, q_len, n_q, d = q.shape
-    num_blocks, n_kv, bs, d2 = k_pool.shape
-    if d2 != d or v_pool.shape != k_pool.shape or out.shape != q.shape or \
-            masks.shape != q.shape[:2] or block_tables.shape[0] != num_seqs or \
-            context_lens.shape != q.shape[:1] or \
-            (tree_lens is not None and tree_lens.shape != q.shape[:1]):
+    dev = _on_device(q, out, k_pool, v_pool, block_tables, context_lens, masks, tree_lens,
+                     workspace, dev_err)
+    qs, ks = q.shape, k_pool.shape
+    num_seqs, q_len, n_q, d = qs
+    num_blocks, n_kv, bs, d2 = ks
+    seqs, rows = (num_seqs,), (num_seqs, q_len)
+    if d2 != d or v_pool.shape != ks or out.shape != qs or masks.shape != rows or \
+            block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or \
+            context_lens.shape != seqs or (tree_lens is not None and tree_lens.shape != seqs):
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_tree shapes")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or \
             (tree_lens is not None and tree_lens.dtype != torch.int32):
@@ -288,13 +300,11 @@ def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, sc
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_tree dtypes")
     if workspace is None:
         workspace = alloc_tree_workspace(q, k_pool)
-    with _current(q.device):
-        _check(lib.pa_decode_tree(
-            _p(out), _p(q), _p(k_pool), _p(v_pool), _p(block_tables), _p(context_lens), _p(masks),
-            _p(tree_lens), float(scale), bs, n_q, n_kv, d, num_seqs, q_len,
-            block_tables.shape[1], num_blocks, dtype_code(q), dtype_code(k_pool), float(k_scale),
-            float(v_scale), _p(workspace), workspace.numel() * workspace.element_size(),
-            _p(dev_err), _stream(stream, q.device)), "pa_decode_tree")
+    _launch(dev, stream, "pa_decode_tree", lib.pa_decode_tree, out.data_ptr(), q.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), masks.data_ptr(), _ptr(tree_lens), scale, bs, n_q, n_kv, d,
+            num_seqs, q_len, block_tables.shape[1], num_blocks, dtype_code(q), dtype_code(k_pool),
+            k_scale, v_scale, workspace.data_ptr(), workspace.nbytes, _ptr(dev_err))
     return out
 
 
@@ -443,7 +453,7 @@ def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream
     query_start_loc[s] .. query_start_loc[s + 1] - 1 (int32, on the device).
     q, k and v may be strided along the tokens (parts of one projection)."""
     _contig(out, query_start_loc)
-    _on_device(q, out, k, v, query_start_loc, dev_err)
+    dev = _on_device(q, out, k, v, query_start_loc, dev_err)
     total, n_q, d = q.shape
     n_kv = k.shape[1]
     if out.shape != q.shape or k.shape != (total, n_kv, d) or v.shape != k.shape or \
@@ -454,17 +464,15 @@ def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream
     if not out.dtype == q.dtype == k.dtype == v.dtype:
         raise PAError(PA_ERR_INVALID_ARG, "pa_prefill_packed dtypes")
     strides = []
-    for t in (q, k, v):
+    for t, heads in ((q, n_q), (k, n_kv), (v, n_kv)):
         st = t.stride()
-        if st[2] != 1 and d > 1 or st[1] != d and t.shape[1] > 1:
+        if st[2] != 1 and d > 1 or st[1] != d and heads > 1:
             raise PAError(PA_ERR_INVALID_ARG, "a token's heads must be contiguous")
         # a single token's stride is never used
-        strides.append(st[0] if total > 1 else t.shape[1] * d)
-    with _current(q.device):
-        _check(lib.pa_prefill_packed(_p(out), _p(q), _p(k), _p(v), _p(query_start_loc),
-                                     float(scale), n_q, n_kv, d, query_start_loc.shape[0] - 1,
-                                     total, *strides, dtype_code(q), _p(dev_err),
-                                     _stream(stream, q.device)), "pa_prefill_packed")
+        strides.append(st[0] if total > 1 else heads * d)
+    _launch(dev, stream, "pa_prefill_packed", lib.pa_prefill_packed, out.data_ptr(), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), query_start_loc.data_ptr(), scale, n_q, n_kv, d,
+            query_start_loc.shape[0] - 1, total, *strides, dtype_code(q), _ptr(dev_err))
     return out
 
 
@@ -520,12 +528,15 @@ def _pool_pointers(pools):
     """(array of pool pointers, layers, one layer's shape, dtype, device) of a
     list of per-layer pools or one [n_layers, ...] tensor."""
     if isinstance(pools, torch.Tensor):
-        if pools.dim() != 5 or (pools.shape[0] and not pools[0].is_contiguous()):
+        shape, st = pools.shape, pools.stride()
+        if len(shape) != 5 or shape[0] and (
+                st[4] != 1 or st[3] != shape[4] or st[2] != shape[3] * st[3] or
+                st[1] != shape[2] * st[2]):
             raise PAError(PA_ERR_INVALID_ARG, "pools must be [n_layers, num_blocks, n_kv, 16, d], "
                                               "each layer contiguous")
-        n, base, step = pools.shape[0], pools.data_ptr(), pools.stride(0) * pools.element_size()
-        return (ctypes.c_void_p * max(n, 1))(*[base + i * step for i in range(n)]), n, \
-            pools.shape[1:], pools
+        n, base, step = shape[0], pools.data_ptr(), st[0] * pools.element_size()
+        return (ctypes.c_void_p * max(n, 1))(*range(base, base + n * step, step) if step else
+                                             [base] * n), n, shape[1:], pools
     _contig(*pools)
     for t in pools:
         if t.shape != pools[0].shape or t.dtype != pools[0].dtype or t.dim() != 4:
@@ -551,20 +562,21 @@ def pa_compact_tokens(k_pools, v_pools, block_tables, context_lens, tree_lens, a
     ints = (block_tables, context_lens, accepted, accepted_lens) + \
         (() if tree_lens is None else (tree_lens,))
     _contig(*ints)
-    _on_device(kt, vt, dev_err, *ints)
-    if any(t.dtype != torch.int32 for t in ints) or kt.dtype != vt.dtype:
-        raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens dtypes (index tensors: int32)")
+    dev = _on_device(kt, vt, dev_err, *ints)
+    for t in ints:
+        if t.dtype != torch.int32:
+            raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens: index tensors must be int32")
+    if kt.dtype != vt.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens dtypes")
     num_seqs, max_accepted = accepted.shape
     if block_tables.shape[0] != num_seqs or any(
             t.shape != (num_seqs,) for t in (context_lens, accepted_lens) + ints[4:]):
         raise PAError(PA_ERR_INVALID_ARG, "pa_compact_tokens shapes")
     num_blocks, n_kv, bs, d = shape
-    with _current(kt.device):
-        _check(lib.pa_compact_tokens(kp, vp, n_layers, _p(block_tables), _p(context_lens),
-                                     _p(tree_lens), _p(accepted), _p(accepted_lens), num_seqs,
-                                     int(q_len), max_accepted, block_tables.shape[1], n_kv, d, bs,
-                                     num_blocks, dtype_code(kt), _p(dev_err),
-                                     _stream(stream, kt.device)), "pa_compact_tokens")
+    _launch(dev, stream, "pa_compact_tokens", lib.pa_compact_tokens, kp, vp, n_layers,
+            block_tables.data_ptr(), context_lens.data_ptr(), _ptr(tree_lens),
+            accepted.data_ptr(), accepted_lens.data_ptr(), num_seqs, int(q_len), max_accepted,
+            block_tables.shape[1], n_kv, d, bs, num_blocks, dtype_code(kt), _ptr(dev_err))
 
 
 # --------------------------------------------------------------------------

@@ -387,12 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool bad;
         it.len = seq_span(p, max(seq, 0), it.start, bad);
-        it.i0 = level * span;
+        // of an odd number of tiles the first, which sees the fewest keys, is
+        // alone in its item
+        const bool odd = ((it.len + QT - 1) >> (lspan - 1)) & 1;
+        it.i0 = max(0, level * span - (odd ? QT : 0));
         it.h0 = (int)(idx - want * hgroups) << lhb;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int i = it.i0 + x * QT;
-          it.nkt[x] = i < it.len ? (min(it.len, i + QT) + kTileN - 1) / kTileN : 0;
+          it.nkt[x] = i < it.len && !(x == 1 && odd && level == 0)
+                          ? (min(it.len, i + QT) + kTileN - 1) / kTileN
+                          : 0;
         }
       }
       const int slot = k % kItems;
@@ -546,9 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool BF16, int D>
 cudaError_t launch_t(const PromptParams& p, const CUtensorMap* tmq, const CUtensorMap* tmk,
                      const CUtensorMap* tmv, cudaStream_t st) {
-  const cudaError_t attr = cudaFuncSetAttribute(
-      prompt_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<unsigned long long> set{0};
+  const cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(prompt_kernel<BF16, D>), Lay<D>::kSmem, set);
+  if (e != cudaSuccess) return e;
   // no more CTAs than there can be items
   const int span = 2 * (kTileM >> p.log2_hb);
   const long long most = ((long long)p.total / span + p.num_seqs) * (p.n_q >> p.log2_hb);

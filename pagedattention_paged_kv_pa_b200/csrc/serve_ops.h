@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/pa.h"
@@ -14,6 +15,10 @@ namespace pa {
 
 // SMs of the current device.
 int device_sms();
+
+// Allows `bytes` of dynamic shared memory to a kernel on the current device;
+// `done` (one per kernel, zero at first) remembers the devices it was set on.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
 // Whole-prompt attention: sequence s owns rows query_start_loc[s] ..
 // query_start_loc[s + 1] - 1 of q, k, v and out.

@@ -948,8 +948,9 @@ cudaError_t launch_t(const TreeParams& p, const CUtensorMap* tmq, const CUtensor
                      const CUtensorMap* tmv, cudaStream_t st) {
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   using L = Lay<D, FP8, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(tree_kernel<BF16, D, FP8, SPLIT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  static std::atomic<unsigned long long> set{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_kernel<BF16, D, FP8, SPLIT>),
+                             L::kSmem, set);
   if (e != cudaSuccess) return e;
   int shares = device_sms() < kTreeCtas ? device_sms() : kTreeCtas;
   shares /= p.row_groups;
