@@ -52,6 +52,7 @@ struct TreeParams {
   float2* ws_ml;   // [CTA][2 slots][rows] (log2-domain maximum, sum)
   int row_groups;  // CTAs side by side over the same keys
   int step_keys, log2_step;  // keys of a step of the work split
+  int seg_cost;    // fixed costs of a unit, in steps
 };
 constexpr int kTreeCtas = 148;  // most CTAs of a launch: the workspace is laid out for them
 size_t tree_ws_bytes(int q_len, int group, int D);

@@ -19,7 +19,7 @@
 //    reader of a K/V tile finds it in L2).
 //
 // Work split.  Persistent CTAs.  The (sequence, kv head) units lie end to end,
-// measured in key steps (256 keys when split, else 128) plus kSegCost steps'
+// measured in key steps (256 keys when split, else 128) plus seg_cost steps'
 // worth of time for a unit's fixed costs; share c of C is [c T / C, (c + 1) T /
 // C) of the total T.  A run of a unit's steps inside one share is a segment.  A
 // segment that is the whole unit writes the output; others write their
@@ -34,7 +34,7 @@
 // warp 11 walks the share.  E4M3 caches: warps 9 and 10 bring raw rows into
 // rings of raw tiles, and warps 12-15 widen K, 16-19 V to the f16 operands
 // (code x 2^-8, exact, undone by the score and output scales); the
-// softmax threads write their query rows, scaled by a power of two into f16's
+// K converters also write the query rows, scaled by a power of two into f16's
 // range when they are bf16, and P is f16.  Every wait is bounded; a role that
 // gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its loads
 // and MMAs and frees TMEM.
@@ -54,7 +54,6 @@ constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
 constexpr int kSegs = 4;  // segments scheduled ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMergeRows = 16;  // rows of a merge CTA
-constexpr int kSegCost = 1;  // a unit's fixed costs, in steps
 
 template <int D, bool FP8, bool SPLIT>
 struct Lay {
@@ -71,7 +70,8 @@ struct Lay {
   static constexpr int kRawOff = kVOff + kVS * kOp;
   static constexpr int kRedOff = kRawOff + 2 * kRS * kRaw;  // [2][128] float2
   static constexpr int kBarOff = kRedOff + (SPLIT ? 2048 : 0);
-  static constexpr int kSmem = kBarOff + 1024;
+  static constexpr int kExpOff = kBarOff + 768;  // E4M3: the query rows' exponents, int8
+  static constexpr int kSmem = kExpOff + 256 * kQ;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   // TMEM columns: S_A 0, S_B 128; a 64-wide head leaves room for P beside S, so
   // that S of the next tile is made while the softmax works on this one
@@ -80,7 +80,7 @@ struct Lay {
   static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
   // The o-th product of a step: true for S, false for O += P V, of tile x.  A
   // segment's first step ends the one before, whose last products do not wait
-  // for the new Q (which, for E4M3, the softmax threads write after them).
+  // for the new Q.
   // Where P lies over S, S of the next tile comes after O += P V (the tensor
   // core keeps their order); else before it.
   static __device__ __forceinline__ bool op_at(int j, int o, int& x) {
@@ -113,7 +113,7 @@ struct Bars {
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= 1024, "barriers");
+static_assert(sizeof(Bars) <= 768, "barriers");
 
 using attn::wait_all;
 using attn::wait_ok;
@@ -142,14 +142,16 @@ __device__ __forceinline__ int seq_steps(const TreeParams& p, int s) {
   const int n = seq_nodes(p, s), c = seq_ctx(p, s);
   return n > 0 ? (c + p.step_keys - 1) >> p.log2_step : 0;
 }
-__device__ __forceinline__ int weight(int steps) { return steps > 0 ? steps + kSegCost : 0; }
+__device__ __forceinline__ int weight(const TreeParams& p, int steps) {
+  return steps > 0 ? steps + p.seg_cost : 0;
+}
 
 // T, by one warp; `first` gets the weight of sequence `lane`; flags lengths out
 // of range when `report`
 __device__ long long total_weight(const TreeParams& p, int lane, bool report, int& first) {
-  long long part = first = lane < p.num_seqs ? weight(seq_steps(p, lane)) : 0;
+  long long part = first = lane < p.num_seqs ? weight(p, seq_steps(p, lane)) : 0;
 #pragma unroll 1
-  for (int s = 32 + lane; s < p.num_seqs; s += 32) part += weight(seq_steps(p, s));
+  for (int s = 32 + lane; s < p.num_seqs; s += 32) part += weight(p, seq_steps(p, s));
   if (report) {
     int err = 0;
 #pragma unroll 1
@@ -186,7 +188,7 @@ __device__ bool locate(const TreeParams& p, long long X, int lane, int first, in
 #pragma unroll 1
   for (int base = 0; base < p.num_seqs; base += 32) {
     const int s = base + lane;
-    const int n = base == 0 ? first : (s < p.num_seqs ? weight(seq_steps(p, s)) : 0);
+    const int n = base == 0 ? first : (s < p.num_seqs ? weight(p, seq_steps(p, s)) : 0);
     int incl = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -269,6 +271,36 @@ __device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int
       for (int h = 0; h < D / 64; ++h)
         tma_load_2d_hint(dst + h * 16384 + lane * 2048, map, full, 64 * h, y, policy);
     }
+  }
+}
+
+// A query row as the f16 operand row `r` of an E4M3 cache's products: a bf16 row
+// is multiplied by 2^e first, e left in *exponent for its scores; no row (null):
+// zeros.
+template <bool BF16, int D>
+__device__ __forceinline__ void write_query_row(uint8_t* tile, int r, const void* row,
+                                                int8_t* exponent) {
+  const uint4* src = static_cast<const uint4*>(row);
+  int e = 0;
+  if constexpr (BF16) {
+    uint32_t mag = 0;
+#pragma unroll 4
+    for (int ch = 0; ch < D / 8; ++ch) {
+      const uint4 v = row ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+      mag = max(max(mag, max(bf16x2_max_mag(v.x), bf16x2_max_mag(v.y))),
+                max(bf16x2_max_mag(v.z), bf16x2_max_mag(v.w)));
+    }
+    e = f16_row_shift(mag);
+  }
+  *exponent = (int8_t)e;
+  const float up = exp2i(e);
+#pragma unroll 4
+  for (int ch = 0; ch < D / 8; ++ch) {
+    uint4 v = row ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+    if constexpr (BF16)
+      v = make_uint4(bf16x2_to_f16x2_scaled(v.x, up), bf16x2_to_f16x2_scaled(v.y, up),
+                     bf16x2_to_f16x2_scaled(v.z, up), bf16x2_to_f16x2_scaled(v.w, up));
+    *reinterpret_cast<uint4*>(tile + op_off(r, ch)) = v;
   }
 }
 
@@ -540,15 +572,15 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       bool more = sc < sh.C && gbeg < gend && locate(p, gbeg, lane, first, s, gs, w);
       if (more) {
         h = quotient(gbeg - gs, w);
-        step = max(0, (int)(gbeg - gs - (long long)h * w) - kSegCost);
+        step = max(0, (int)(gbeg - gs - (long long)h * w) - p.seg_cost);
       }
       for (int k = 0;;) {
         Seg g;
         g.s = -1;
         bool emit = !more;
         if (more) {
-          const int steps = w - kSegCost;
-          const long long u = gs + (long long)h * w + kSegCost;  // of the unit's first step
+          const int steps = w - p.seg_cost;
+          const long long u = gs + (long long)h * w + p.seg_cost;  // of the unit's first step
           if (u + step >= gend) {
             more = false;
             continue;
@@ -571,7 +603,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             gs += (long long)p.n_kv * w;
             do {
               ++s;
-              w = s < p.num_seqs ? weight(seq_steps(p, s)) : 0;
+              w = s < p.num_seqs ? weight(p, seq_steps(p, s)) : 0;
             } while (s < p.num_seqs && w == 0);
             more = s < p.num_seqs;
           }
@@ -600,9 +632,31 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       Seg g;
       bool ok = true;
       uint32_t c = 0;
+      int nq[2] = {0, 0};
       while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
+        // the K converters write the segment's query rows first
+#pragma unroll
+        for (int x = 0; x < L::kQ; ++x) {
+          const int nodes = tile_nodes(g, x);
+          if (vop || !ok || nodes == 0) continue;
+          // the rows of the segment before are done with, and the exponents of
+          // the one before that
+          if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
+          if (nq[x] > 1) ok = ok && wait_all(&B->o_free[x], nq[x] & 1, B, p.dev_err);
+          if (!ok) continue;
+          const int ri = ct / G, node = (SPLIT ? 0 : 2 * rg + x) * QT + ri;
+          write_query_row<BF16, D>(
+              smem + L::kQOff + x * L::kOp, ct,
+              ri < nodes ? static_cast<const T16*>(p.q) +
+                               (((size_t)g.s * p.q_len + node) * p.n_q + g.h * G + ct - ri * G) * D
+                         : nullptr,
+              reinterpret_cast<int8_t*>(smem + L::kExpOff) + ((nq[x] & 1) * L::kQ + x) * 128 + ct);
+          tc::fence_async_smem();
+          mbar_arrive(&B->q_full[x]);
+          ++nq[x];
+        }
         for (int t = g.t0; t < g.t1 && ok; ++t, ++c) {
           const int st = c % NS, rs = c % RS;
           bool w = wait_ok(&B->raw_full[vop][rs], (c / RS) & 1, B, p.dev_err);
@@ -672,38 +726,11 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       uint64_t mask = valid ? __ldg(&p.masks[(size_t)g.s * p.q_len + node]) : 0ull;
       if (g.n < 64) mask &= (1ull << g.n) - 1ull;
       float sl = p.scale_log2;
-      if constexpr (FP8) {
-        // the query row as f16: a bf16 row times 2^e, its scores times 2^-e
-        uint4 v[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T16*>(p.q) + row * D);
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) v[ch] = valid ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
-        if constexpr (BF16) {
-          uint32_t mag = 0;
-#pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch)
-            mag = max(max(mag, max(bf16x2_max_mag(v[ch].x), bf16x2_max_mag(v[ch].y))),
-                      max(bf16x2_max_mag(v[ch].z), bf16x2_max_mag(v[ch].w)));
-          const int e = f16_row_shift(mag);
-          const float up = exp2i(e);
-          sl *= exp2i(-e);
-#pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch)
-            v[ch] = make_uint4(
-                bf16x2_to_f16x2_scaled(v[ch].x, up), bf16x2_to_f16x2_scaled(v[ch].y, up),
-                bf16x2_to_f16x2_scaled(v[ch].z, up), bf16x2_to_f16x2_scaled(v[ch].w, up));
-        }
-        if (!SPLIT || x == 0) {
-          if (seg > 0)
-            ok = wait_all(&B->q_empty[x], (seg - 1) & 1, B, p.dev_err);
-          if (!ok) break;
-          uint8_t* d = smem + L::kQOff + x * L::kOp;
-#pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch)
-            *reinterpret_cast<uint4*>(d + op_off(r, ch)) = v[ch];
-          tc::fence_async_smem();
-          mbar_arrive(&B->q_full[x]);
-        }
+      if constexpr (FP8) {  // the row went in times 2^e
+        ok = wait_all(&B->q_full[SPLIT ? 0 : x], seg & 1, B, p.dev_err);
+        if (!ok) break;
+        sl *= exp2i(-reinterpret_cast<int8_t*>(
+            smem + L::kExpOff)[((seg & 1) * L::kQ + (SPLIT ? 0 : x)) * 128 + r]);
       }
       const int P = g.ctx - g.n;  // keys before the tree; may be negative
       float m = -INFINITY, l = 0.f;
@@ -882,7 +909,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
       long long gs;
       if (locate(p, X, lane, first, s0, gs, w)) {
         h = quotient(X - gs, w);
-        const long long u = gs + (long long)h * w + kSegCost, end = u + w - kSegCost;
+        const long long u = gs + (long long)h * w + p.seg_cost, end = u + w - p.seg_cost;
         if (u < X && u >= sh.start(c)) {
           s = s0;
           // the last share with steps of the unit
@@ -997,6 +1024,7 @@ cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspa
   p.row_groups = tiles > 2 ? 2 : 1;
   p.step_keys = tiles == 1 ? 2 * kTileN : kTileN;
   p.log2_step = tiles == 1 ? 8 : 7;
+  p.seg_cost = fp8 ? 2 : 1;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (size_t)kTreeCtas * 2 * (tiles == 1 ? 128 : 256) * D);
   if (D == 128)
