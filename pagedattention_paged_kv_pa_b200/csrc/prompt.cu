@@ -21,9 +21,9 @@
 // other warps.
 //
 // Roles: warps 0-3 softmax of tile A, warps 4-7 of tile B (one thread per
-// row, its 128 scores in registers), warp 8 owns TMEM and issues the MMAs,
-// warp 9 loads Q, K and V by TMA (K and V share a ring of stages), warp 10
-// schedules, warp 11 zeroes the rows of an item's last V tile that lie behind
+// row, its 128 scores in registers), warps 8 and 9 issue the MMAs of A and B,
+// warp 10 loads Q, K and V by TMA (K and V share a ring of stages), warp 11
+// schedules, warp 12 zeroes the rows of an item's last V tile that lie behind
 // its sequence (another sequence's values or padding: 0 x NaN must not reach
 // O).  Every wait is bounded; a role that gives up flags PA_DEVERR_TIMEOUT and
 // leaves, and the CTA drains its loads and MMAs and frees TMEM.
@@ -39,10 +39,10 @@ namespace {
 using attn::kTileM;
 using attn::kTileN;
 
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;  // and 11: see the roles
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 11, kFixWarp = 12;  // 13-15 idle
 constexpr int kItems = 4;              // items scheduled ahead
-constexpr uint32_t kItemReaders = 11;  // 8 softmax warps, MMA, loads, fixer
+constexpr uint32_t kItemReaders = 12;  // 8 softmax warps, 2 MMA, loads, fixer
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 10;
 
@@ -59,15 +59,6 @@ struct Lay {
   static constexpr bool kSepP = D == 64;
   static constexpr int tP(int x) { return kSepP ? 256 + 64 * x : 128 * x; }
   static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
-  // The o-th product of a step: true for S, false for O += P V, of tile x.  An
-  // item's first step ends the item before, whose last products do not wait
-  // for the new Q.  Where P lies over S, S of the next tile comes after O += P V
-  // (the tensor core keeps their order); else before it.
-  static __device__ __forceinline__ bool op_at(int j, int o, int& x) {
-    const bool pairs = j == 0 || kSepP;  // both of one kind, then both of the other
-    x = pairs ? o & 1 : o >> 1;
-    return pairs ? (o >> 1) == (j == 0 ? 1 : 0) : (o & 1) == 1;
-  }
   static_assert(kStages <= kMaxStages, "stage barriers");
 };
 
@@ -81,11 +72,11 @@ struct Item {
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t raw[kMaxStages];  // a V tile whose tail warp 11 has yet to zero
+  uint64_t raw[kMaxStages];  // a V tile whose tail warp 12 has yet to zero
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
   uint64_t s_empty[2], pv_done[2];  // P beside S only
-  uint64_t done;
+  uint64_t done[2], turn[2];
   Item items[kItems];
   uint32_t tmem_base;
   int abort_flag;
@@ -134,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&B->full[s], 1);
-      mbar_init(&B->empty[s], 1);
+      mbar_init(&B->empty[s], 2);
       mbar_init(&B->raw[s], 1);
     }
     for (int s = 0; s < kItems; ++s) {
@@ -142,6 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->item_empty[s], kItemReaders);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&B->done[x], 1);
+      mbar_init(&B->turn[x], 1);
       mbar_init(&B->q_full[x], 1);
       mbar_init(&B->q_empty[x], 1);
       mbar_init(&B->s_full[x], 1);
@@ -152,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->o_full[x], 1);
       mbar_init(&B->o_free[x], 128);
     }
-    mbar_init(&B->done, 1);
     B->abort_flag = 0;
     fence_mbar_init();
   }
@@ -167,116 +159,108 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = B->tmem_base;
 
-  // 384 threads at 168 registers: 64,512 = 256 x 192 + 128 x 120
+  // 512 threads at 128 registers: 65,536 = 256 x 192 + 256 x 64
   if (warp >= kMmaWarp) {
-  tc::regs_dec<120>();
-  if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // per key tile j and X = A, B: O_X += P_X V of tile j - 1 and S_X = Q_X K^T
-    // of tile j, in the order of op_at.  The whole warp walks the tiles and
-    // waits; one lane issues.  One copy of each product's code: unrolled copies
-    // miss the instruction cache.
+  tc::regs_dec<64>();
+  if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ------------------------------------------------------------ MMA issuers
+    // one warp per tile X: per key tile j, O_X += P_X V of tile j - 1 and S_X =
+    // Q_X K^T of tile j (in this order where P lies over S: the tensor core
+    // keeps it; else S first).  The whole warp walks the tiles and waits, one
+    // lane issues.  The waits of one warp run while the other's MMAs do; they
+    // take turns, so that one's batch is not spread over the other's and the
+    // softmax passes of A and B fall into opposite phases.
     constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
     constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
-    const uint64_t dQ = tc::smem_desc(sbase + L::kQOff), dK = tc::smem_desc(sbase + L::kKVOff),
-                   dV = tc::smem_desc(sbase + L::kKVOff, 16384);
     constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
+    const int x = warp - kMmaWarp;
+    const uint64_t dQ = tc::smem_desc(sbase + L::kQOff + x * L::kOp),
+                   dK = tc::smem_desc(sbase + L::kKVOff),
+                   dV = tc::smem_desc(sbase + L::kKVOff, 16384);
+    const uint32_t tS = tmem + x * 128, tP = tmem + L::tP(x), tO = tmem + L::tO(x);
     Reader rd;
     Item it;
-    bool ok = true, issued = false, more = true;
+    bool ok = true, issued = false;
     uint32_t c = 0;  // stages used before this tile: K of tile j in c, V in c + 1
-    int items0 = 0, items1 = 0, s0 = 0, s1 = 0, p0 = 0, p1 = 0, o0 = 0, o1 = 0;
-    int pj = -1, pn0 = 0, pn1 = 0;  // the tile before, and its item's tiles of A and B
-    while (ok && more) {
-      more = __all_sync(0xffffffffu, rd.next(B, p.dev_err, it));
-      if (more && lane == 0) rd.done(B);
+    uint32_t items = 0, tiles = 0, turns = 0;
+    auto scores = [&](uint64_t k, bool last) {
+      tc::fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+          tc::mma(tS, dQ + off, k + off, idesc_s, kk > 0);
+        }
+        tc::commit(&B->s_full[x]);
+        if (last) tc::commit(&B->q_empty[x]);
+      }
       __syncwarp();
-      // after the last item one more step, for the products still to do
-      const int n0 = more ? it.nkt[0] : 0, n1 = more ? it.nkt[1] : 0, n = max(max(n0, n1), 1);
-      for (int j = 0; j < n && ok; ++j) {
+    };
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+      if (lane == 0) rd.done(B);
+      __syncwarp();
+      const int n = max(it.nkt[0], it.nkt[1]), mine = x ? it.nkt[1] : it.nkt[0];
+      if (mine > 0) ok = wait_all(&B->q_full[x], items & 1, B, p.dev_err);
+      for (int j = 0; j <= n && ok; ++j, c += 2, ++turns) {
         const uint32_t cv = c - 1;
         const int sk = c % NS, sv = cv % NS;
-        // what the next MMAs read besides P has usually landed long before P
-        // is written: waited for first, off the chain P -> O += P V -> S
-        if (pj >= 0) ok = wait_all(&B->full[sv], (cv / NS) & 1, B, p.dev_err);
-        if (more && j > 0) ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
-#pragma unroll 1
-        for (int o = 0; o < 4 && ok; ++o) {
-          int x;
-          if (L::op_at(j, o, x)) {
-            const int nx = x ? n1 : n0;
-            if (j >= nx) continue;
-            const int tiles = x ? s1 : s0;
-            if (j == 0) {
-              ok = wait_all(&B->q_full[x], (x ? items1 : items0) & 1, B, p.dev_err);
-              ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
-              x ? ++items1 : ++items0;
-            }
-            if (L::kSepP && tiles > 0)  // the softmax has read S of the tile before
-              ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
-            if (tc::elect_one()) {
-              const uint64_t q = dQ + x * kOpStep, k = dK + sk * kOpStep;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-                tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
-              }
-              tc::commit(&B->s_full[x]);
-              // the K tile's last reader of the two
-              if (x == 1 || j >= n1) tc::commit(&B->empty[sk]);
-              if (j == nx - 1) tc::commit(&B->q_empty[x]);
-            }
-            __syncwarp();
-            issued = true;
-            x ? ++s1 : ++s0;
-          } else {
-            const int nx = x ? pn1 : pn0;
-            if (pj < 0 || pj >= nx) continue;
-            const int before = x ? o1 : o0, par = (x ? p1 : p0) & 1;
-            if (pj == 0) {
-              if (before > 0) ok = wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
-              x ? ++o1 : ++o0;
-            }
-            const uint64_t v = dV + sv * kOpStep;
-            const uint32_t tP = tmem + L::tP(x), tO = tmem + L::tO(x);
-            // 16 keys a step = two 8-row groups of V
-            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (pj == 0 && kk == 0) ? 0u : 1u);
-            }
-            __syncwarp();
-            ok = wait_all(&B->p_full[x], par, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int kk = 4; kk < 8; ++kk)
-                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
-              if (x == 1 || pj >= pn1) tc::commit(&B->empty[sv]);
-              if (L::kSepP) tc::commit(&B->pv_done[x]);
-              if (pj == nx - 1) tc::commit(&B->o_full[x]);
-            }
-            __syncwarp();
-            x ? ++p1 : ++p0;
-          }
+        const bool do_pv = j > 0 && j <= mine, do_s = j < mine;
+        const uint64_t v = dV + sv * kOpStep, k = dK + sk * kOpStep;
+        const uint32_t par = (tiles - 1) & 1;
+        if (j > 0) ok = wait_all(&B->full[sv], (cv / NS) & 1, B, p.dev_err);
+        if (j < n) ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+        if (L::kSepP && do_s) {  // S beside P: as soon as the softmax has read the last S
+          if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+          if (!ok) break;
+          scores(k, j == mine - 1);
         }
-        pj = j;
-        pn0 = n0;
-        pn1 = n1;
-        c += 2;
+        if (do_pv) {
+          if (j == 1 && items > 0)
+            ok = ok && wait_all(&B->o_free[x], (items - 1) & 1, B, p.dev_err);
+          ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+        }
+        if (!L::kSepP && (x > 0 || turns > 0))
+          ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+        if (!ok) break;
+        if (do_pv) {
+          tc::fence_after();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
+              tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (j == 1 && kk == 0) ? 0u : 1u);
+          }
+          __syncwarp();
+          ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+            if (L::kSepP) tc::commit(&B->pv_done[x]);
+            if (j == mine) tc::commit(&B->o_full[x]);
+          }
+          __syncwarp();
+        }
+        if (!L::kSepP && do_s) scores(k, j == mine - 1);
+        if (tc::elect_one()) {
+          if (!L::kSepP) mbar_arrive(&B->turn[x ^ 1]);
+          // a stage is free once both warps' MMAs on it are done
+          if (j > 0) tc::commit(&B->empty[sv]);
+          if (j < n) tc::commit(&B->empty[sk]);
+        }
+        __syncwarp();
+        issued = true;
+        tiles += do_s;
       }
+      c -= 2;  // the last step had no K
+      items += mine > 0;
     }
     // everything issued above has completed before TMEM is released
     if (issued) {
-      if (tc::elect_one()) tc::commit(&B->done);
+      if (tc::elect_one()) tc::commit(&B->done[x]);
       __syncwarp();
-      mbar_wait(&B->done, 0);
+      mbar_wait(&B->done[x], 0);
     }
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
@@ -291,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c >= (uint32_t)NS && !wait_ok(&B->empty[st], ((c / NS) - 1) & 1, B, p.dev_err))
           return false;
         uint8_t* d = smem + L::kKVOff + st * L::kOp;
-        // the arrival of a V tile with a tail to zero is warp 11's
+        // the arrival of a V tile with a tail to zero is warp 12's
         uint64_t* bar = tail ? &B->raw[st] : &B->full[st];
         mbar_arrive_expect_tx(bar, L::kOp);
 #pragma unroll
@@ -409,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp == kFixWarp) {
     // ------------------------------------------------- rows behind a sequence
     Reader rd;
     Item it;
