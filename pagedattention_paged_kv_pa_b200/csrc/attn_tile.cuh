@@ -80,27 +80,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (the
-// low bits of x + 1.5 2^23) and f in [-1/2, 1/2]; a degree-3 polynomial with
-// the smallest largest relative error on that interval (2^-13.7, below half a
-// step of f16) gives 2^f, and n is added to its exponent field.  x below -126
-// gives 2^-126 instead of less, so that the exponent field cannot wrap.
-__device__ __forceinline__ void exp2_poly2(float& a, float& b) {
-  const uint64_t x = f2(fmaxf(a, -126.f), fmaxf(b, -126.f));
-  const uint64_t t = add2(x, f2(12582912.f, 12582912.f));
-  const uint64_t n = add2(t, f2(-12582912.f, -12582912.f));
-  const uint64_t f = fma2(n, f2(-1.f, -1.f), x);
-  uint64_t p = fma2(f, f2(0.0551716685295105f, 0.0551716685295105f),
-                    f2(0.2426111251115799f, 0.2426111251115799f));
-  p = fma2(p, f, f2(0.6932609677314758f, 0.6932609677314758f));
-  p = fma2(p, f, f2(0.9999280571937561f, 0.9999280571937561f));
-  float ta, tb, pa, pb;
-  un2(t, ta, tb);
-  un2(p, pa, pb);
-  a = __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
-  b = __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
-}
-
 struct RowState {
   float m, l;  // maximum exponentiated against (log2 units), sum of the weights
 };
@@ -183,9 +162,8 @@ __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
 
 // Weights 2^(x sl - m) of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns
 // their fp32 sum.  Masked scores are -inf, with sl = 1 (tile_max has scaled the
-// others), so that tiles with and without a mask run the same code.  Of every
-// 8 pairs kPoly go through exp2_poly2 (which must not see a masked score).
-template <bool BF16, int kPoly>
+// others), so that tiles with and without a mask run the same code.
+template <bool BF16>
 __device__ __forceinline__ float tile_weights(const float* x, int h, float sl, float neg_m,
                                               uint32_t (&pk)[32]) {
   uint64_t s[2] = {0ull, 0ull};
@@ -194,12 +172,8 @@ __device__ __forceinline__ float tile_weights(const float* x, int h, float sl, f
   for (int c = 0; c < 32; ++c) {
     float a, b;
     un2(fma2(f2(x[64 * h + 2 * c], x[64 * h + 2 * c + 1]), s2, nm), a, b);
-    if ((c & 7) < kPoly) {
-      exp2_poly2(a, b);
-    } else {
-      a = tc::ex2(a);
-      b = tc::ex2(b);
-    }
+    a = tc::ex2(a);
+    b = tc::ex2(b);
     s[c & 1] = add2(s[c & 1], f2(a, b));
     pk[c] = pack2<BF16>(a, b);
   }
@@ -241,8 +215,10 @@ __device__ __forceinline__ void store_rows(uint32_t ta, uint32_t tb, OutT* row, 
   constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
   const int lane = threadIdx.x & 31, q = lane & 3;
   const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
+  const uint32_t rows = __ballot_sync(0xffffffffu, row != nullptr);
 #pragma unroll 1
   for (int hf = 0; hf < 2; ++hf) {  // rows 0 .. 15, then 16 .. 31
+    if ((rows >> (16 * hf) & 0xffffu) == 0) continue;
     uint32_t a[32], b[TWO ? 32 : 1];
     tc::ld16x256b_x8(ta + ((uint32_t)(16 * hf) << 16), a);
     if constexpr (TWO) tc::ld16x256b_x8(tb + ((uint32_t)(16 * hf) << 16), b);

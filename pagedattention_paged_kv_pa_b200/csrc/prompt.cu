@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
           uint32_t pk[32];
-          st.l += attn::tile_weights<BF16, 0>(s, 0, sle, neg_m, pk);
+          st.l += attn::tile_weights<BF16>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
             ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_st();
           tc::fence_before();
           mbar_arrive(&B->p_half[x]);
-          st.l += attn::tile_weights<BF16, 0>(s, 1, sle, neg_m, pk);
+          st.l += attn::tile_weights<BF16>(s, 1, sle, neg_m, pk);
           tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();

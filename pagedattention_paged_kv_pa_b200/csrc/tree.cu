@@ -27,17 +27,17 @@
 // unit began in an earlier share, 1: it ends in a later one), which
 // tree_merge_kernel, a programmatic dependent, combines in share order.
 //
-// Roles: warps 0-3 softmax of A, 4-7 of B (one thread per row), warp 8 owns
-// TMEM and issues the MMAs, warp 9 loads Q and K, warp 10 V (16-token blocks
+// Roles: warps 0-3 softmax of A, 4-7 of B (one thread per row), warps 8 and 9
+// issue the MMAs of A and B, warp 10 loads Q and K, warp 11 V (16-token blocks
 // by TMA through the block table; rows of the block a context ends in are
 // copied, rows past it and blocks with a bad id zeroed by the warp itself),
-// warp 11 walks the share.  E4M3 caches: warps 9 and 10 bring raw rows into
-// rings of raw tiles, and warps 12-15 widen K, 16-19 V to the f16 operands
-// (code x 2^-8, exact, undone by the score and output scales); the
-// K converters also write the query rows, scaled by a power of two into f16's
-// range when they are bf16, and P is f16.  Every wait is bounded; a role that
-// gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its loads
-// and MMAs and frees TMEM.
+// warp 12 walks the share.  E4M3 caches: warp 10 brings raw rows of K and V into
+// rings of raw tiles, warp 11 walks the share, warps 12-15 widen K and 16-19 V
+// to the f16 operands (code x 2^-8, exact, undone by the score and output
+// scales); the K converters also write the query rows, scaled by a power of two
+// into f16's range when they are bf16, and P is f16.  Every wait is bounded; a
+// role that gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its
+// loads and MMAs and frees TMEM.
 #include <type_traits>
 
 #include "attn_tile.cuh"
@@ -50,7 +50,13 @@ namespace {
 using attn::kTileM;
 using attn::kTileN;
 
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
+// 16-bit caches have a load warp each for K and V (and three idle warps), E4M3
+// caches one for both and the converters
+constexpr int kMmaWarp = 8, kKWarp = 10, kConvWarp = 12;
+template <bool FP8>
+constexpr int kVWarp = FP8 ? -1 : 11;
+template <bool FP8>
+constexpr int kSchedWarp = FP8 ? 11 : 12;
 constexpr int kSegs = 4;  // segments scheduled ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMergeRows = 16;  // rows of a merge CTA
@@ -62,7 +68,7 @@ struct Lay {
   static constexpr int kQ = SPLIT ? 1 : 2;    // Q tiles
   static constexpr int kScale = 128 / D;
   static constexpr int kKS = (FP8 ? 2 : 3) * kScale;
-  static constexpr int kVS = (FP8 && !SPLIT && D == 128 ? 1 : 2) * kScale;
+  static constexpr int kVS = (FP8 ? (SPLIT || D == 64 ? 2 : 1) : (SPLIT ? 3 : 2)) * kScale;
   static constexpr int kRS = FP8 ? 2 * kScale : 0;  // raw K stages, and raw V stages
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kQ * kOp;
@@ -78,22 +84,12 @@ struct Lay {
   static constexpr bool kSepP = D == 64;
   static constexpr int tP(int x) { return kSepP ? 256 + 64 * x : 128 * x; }
   static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
-  // The o-th product of a step: true for S, false for O += P V, of tile x.  A
-  // segment's first step ends the one before, whose last products do not wait
-  // for the new Q.
-  // Where P lies over S, S of the next tile comes after O += P V (the tensor
-  // core keeps their order); else before it.
-  static __device__ __forceinline__ bool op_at(int j, int o, int& x) {
-    const bool pairs = j == 0 || kSepP;  // both of one kind, then both of the other
-    x = pairs ? o & 1 : o >> 1;
-    return pairs ? (o >> 1) == (j == 0 ? 1 : 0) : (o & 1) == 1;
-  }
-  static constexpr int kThreads = FP8 ? 640 : 384;
-  // registers: 640 x 96 = 61,440 = 256 x 128 + 384 x 72 + 1,024, or 384 x 168 =
-  // 64,512 = 256 x 192 + 128 x 120
-  static constexpr int kSoftRegs = FP8 ? 128 : 192, kOtherRegs = FP8 ? 72 : 120;
-  // readers of a segment: 8 softmax warps, MMA, K and V loads, 8 converters
-  static constexpr uint32_t kReaders = FP8 ? 19 : 11;
+  static constexpr int kThreads = FP8 ? 640 : 512;
+  // registers: 640 x 96 = 61,440 = 256 x 128 + 384 x 72 + 1,024, or 512 x 128 =
+  // 65,536 = 256 x 184 + 256 x 72
+  static constexpr int kSoftRegs = FP8 ? 128 : 184, kOtherRegs = FP8 ? 72 : 72;
+  // readers of a segment: 8 softmax warps, 2 MMA, 2 loads or 1 and 8 converters
+  static constexpr uint32_t kReaders = FP8 ? 19 : 12;
 };
 
 struct Seg {
@@ -104,11 +100,11 @@ struct Seg {
 };
 
 struct Bars {
-  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], raw_full[2][4], raw_empty[2][4];
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], raw_full[2][4], raw_empty[2][4];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], red[2];
   uint64_t s_empty[2], pv_done[2];  // P beside S only
-  uint64_t done;
+  uint64_t done[2], turn[2];
   Seg segs[kSegs];
   uint32_t tmem_base;
   int abort_flag;
@@ -314,7 +310,7 @@ __device__ __forceinline__ uint32_t seen_bits(int first, int P, uint64_t mask) {
 }
 
 template <bool BF16, int D, bool FP8, bool SPLIT>
-__global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
+__global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
     tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -336,11 +332,11 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
       mbar_init(&B->k_full[s], FP8 ? 128 : 1);
-      mbar_init(&B->k_empty[s], 1);
+      mbar_init(&B->k_empty[s], SPLIT ? 1 : 2);
     }
     for (int s = 0; s < VS; ++s) {
       mbar_init(&B->v_full[s], FP8 ? 128 : 1);
-      mbar_init(&B->v_empty[s], 1);
+      mbar_init(&B->v_empty[s], SPLIT ? 1 : 2);
     }
     for (int s = 0; s < RS; ++s) {
       for (int v = 0; v < 2; ++v) {
@@ -354,7 +350,9 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&B->q_full[x], FP8 ? 128 : 1);
-      mbar_init(&B->q_empty[x], 1);
+      mbar_init(&B->done[x], 1);
+      mbar_init(&B->turn[x], 1);
+      mbar_init(&B->q_empty[x], SPLIT ? 2 : 1);
       mbar_init(&B->s_full[x], 1);
       mbar_init(&B->p_half[x], 128);
       mbar_init(&B->p_full[x], 128);
@@ -364,7 +362,6 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       mbar_init(&B->o_free[x], SPLIT ? 256 : 128);
       mbar_init(&B->red[x], 128);
     }
-    mbar_init(&B->done, 1);
     B->abort_flag = 0;
     fence_mbar_init();
   }
@@ -381,136 +378,124 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
 
   if (warp >= kMmaWarp) {
     tc::regs_dec<L::kOtherRegs>();
-    if (warp == kMmaWarp) {
-      // ---------------------------------------------------------- MMA issuer
-      // per step j and X = A, B: O_X += P_X V of step j - 1 and S_X = Q_X K^T of
-      // step j, in the order of op_at.  The whole warp walks the steps and
-      // waits; one lane issues.  One copy of each product's code: unrolled
-      // copies miss the instruction cache.
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // --------------------------------------------------------- MMA issuers
+      // one warp per tile X: per step j, O_X += P_X V of step j - 1 and S_X =
+      // Q_X K^T of step j (in this order where P lies over S: the tensor core
+      // keeps it; else S first).  The whole warp walks the steps and waits, one
+      // lane issues.  The waits of one warp run while the other's MMAs do.  Where
+      // A and B share the key tiles and the products bound them they take turns,
+      // so that one's batch is not spread over the other's and their softmax
+      // passes fall into opposite phases.
+      constexpr bool kTurns = !SPLIT && !L::kSepP;
       constexpr uint32_t idesc_s = tc::idesc_f16(kOpBf16, false, kTileM, kTileN);
       constexpr uint32_t idesc_pv = tc::idesc_f16(kOpBf16, true, kTileM, D);
       constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
-      const uint64_t dQ = tc::smem_desc(sbase + L::kQOff), dK = tc::smem_desc(sbase + L::kKOff),
+      const int x = warp - kMmaWarp, qx = SPLIT ? 0 : x;
+      const uint64_t dQ = tc::smem_desc(sbase + L::kQOff + qx * L::kOp),
+                     dK = tc::smem_desc(sbase + L::kKOff),
                      dV = tc::smem_desc(sbase + L::kVOff, 16384);
+      const uint32_t tS = tmem + x * 128, tP = tmem + L::tP(x), tO = tmem + L::tO(x);
       Reader rd;
       Seg g;
-      bool ok = true, issued = false, more = true;
-      uint32_t c = 0, pc = 0;  // key tiles before this segment, and before the last one
-      int segs = 0, items0 = 0, items1 = 0, s0 = 0, s1 = 0, p0 = 0, p1 = 0, o0 = 0, o1 = 0;
-      int pj = -1, pn0 = 0, pn1 = 0;  // the step before, and its segment's steps of A and B
-      while (ok && more) {
-        more = __all_sync(0xffffffffu, rd.next(B, p.dev_err, g));
-        if (more && lane == 0) rd.done(B);
-        __syncwarp();
-        const int nt = more ? g.t1 - g.t0 : 0;
-        const int n0 = SPLIT ? (nt + 1) / 2 : nt;  // A always has a tile
-        const int n1 = SPLIT ? nt / 2 : (more && tile_nodes(g, 1) > 0 ? nt : 0);
-        // after the last segment one more step, for the products still to do
-        const int n = max(n0, 1);
-        for (int j = 0; j < n && ok; ++j) {
-#pragma unroll 1
-          for (int o = 0; o < 4 && ok; ++o) {
-            int x;
-            if (L::op_at(j, o, x)) {
-              const int nx = x ? n1 : n0;
-              if (j >= nx) continue;
-              const int tiles = x ? s1 : s0;
-              if (j == 0) {
-                if (x == 0 || !SPLIT)
-                  ok = wait_all(&B->q_full[x], (SPLIT ? segs : (x ? items1 : items0)) & 1, B,
-                                p.dev_err);
-                x ? ++items1 : ++items0;
-              }
-              const uint32_t tile = c + (SPLIT ? 2 * j + x : j);
-              const int sk = tile % KS;
-              ok = ok && wait_all(&B->k_full[sk], (tile / KS) & 1, B, p.dev_err);
-              if (L::kSepP && tiles > 0)  // the softmax has read S of the tile before
-                ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
-              if (!ok) break;
-              tc::fence_after();
-              if (tc::elect_one()) {
-                const uint64_t q = dQ + (SPLIT ? 0 : x) * kOpStep, k = dK + sk * kOpStep;
+      bool ok = true, issued = false;
+      uint32_t c = 0;  // key tiles before this segment
+      uint32_t segs = 0, items = 0, tiles = 0, turns = 0;
+      auto scores = [&](uint64_t k, bool last) {
+        tc::fence_after();
+        if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-                  tc::mma(tmem + x * 128, q + off, k + off, idesc_s, kk > 0);
-                }
-                tc::commit(&B->s_full[x]);
-                // the K tile's last reader of the two
-                if (SPLIT || x == 1 || n1 == 0) tc::commit(&B->k_empty[sk]);
-                if (SPLIT ? 2 * j + x == nt - 1 : j == nx - 1)
-                  tc::commit(&B->q_empty[SPLIT ? 0 : x]);
-              }
-              __syncwarp();
-              issued = true;
-              x ? ++s1 : ++s0;
-            } else {
-              const int nx = x ? pn1 : pn0;
-              if (pj < 0 || pj >= nx) continue;
-              const uint32_t tile = pc + (SPLIT ? 2 * pj + x : pj);
-              const int sv = tile % VS, par = (x ? p1 : p0) & 1;
-              ok = wait_all(&B->v_full[sv], (tile / VS) & 1, B, p.dev_err);
-              if (pj == 0) {
-                // O_X has been read out as often as there were segments before
-                // (split), or segments with a tile of X
-                const int before = SPLIT ? segs - (j == 0 ? 1 : 0) : (x ? o1 : o0);
-                if (before > 0)
-                  ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
-                x ? ++o1 : ++o0;
-              }
-              const uint64_t v = dV + sv * kOpStep;
-              const uint32_t tP = tmem + L::tP(x), tO = tmem + L::tO(x);
-              ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
-              if (!ok) break;
-              tc::fence_after();
-              if (tc::elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
-                  tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv,
-                             (pj == 0 && kk == 0) ? 0u : 1u);
-              }
-              __syncwarp();
-              ok = wait_all(&B->p_full[x], par, B, p.dev_err);
-              if (!ok) break;
-              tc::fence_after();
-              if (tc::elect_one()) {
-#pragma unroll
-                for (int kk = 4; kk < 8; ++kk)
-                  tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
-                if (SPLIT || x == 1 || pn1 == 0) tc::commit(&B->v_empty[sv]);
-                if (L::kSepP) tc::commit(&B->pv_done[x]);
-                if (pj == nx - 1) tc::commit(&B->o_full[x]);
-              }
-              __syncwarp();
-              x ? ++p1 : ++p0;
-            }
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+            tc::mma(tS, dQ + off, k + off, idesc_s, kk > 0);
           }
-          pj = j;
-          pn0 = n0;
-          pn1 = n1;
-          pc = c;
+          tc::commit(&B->s_full[x]);
+          if (last) tc::commit(&B->q_empty[qx]);
+        }
+        __syncwarp();
+      };
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+        if (lane == 0) rd.done(B);
+        __syncwarp();
+        const int nt = g.t1 - g.t0, n = SPLIT ? (nt + 1) / 2 : nt;  // A always has a tile
+        const int mine = x == 0 ? n : (SPLIT ? nt / 2 : (tile_nodes(g, 1) > 0 ? nt : 0));
+        if (SPLIT || mine > 0)
+          ok = wait_all(&B->q_full[qx], (SPLIT ? segs : items) & 1, B, p.dev_err);
+        // (split: a tile without a step is done with Q)
+        if (SPLIT && mine == 0 && lane == 0) mbar_arrive(&B->q_empty[0]);
+        const uint32_t before = SPLIT ? segs : items;  // O_X read out so often
+        for (int j = 0; j <= n && ok; ++j, ++turns) {
+          const bool do_pv = j > 0 && j <= mine, do_s = j < mine;
+          // split: own key tiles; else A's and B's, a tile of no rows included
+          const uint32_t ck = c + (SPLIT ? 2 * j + x : j), cv = ck - (SPLIT ? 2 : 1);
+          const bool use_k = SPLIT ? do_s : j < n, use_v = SPLIT ? do_pv : j > 0;
+          const int sk = ck % KS, sv = cv % VS;
+          const uint64_t v = dV + sv * kOpStep, k = dK + sk * kOpStep;
+          const uint32_t par = (tiles - 1) & 1;
+          if (use_v) ok = wait_all(&B->v_full[sv], (cv / VS) & 1, B, p.dev_err);
+          if (use_k) ok = ok && wait_all(&B->k_full[sk], (ck / KS) & 1, B, p.dev_err);
+          if (L::kSepP && do_s) {  // S beside P: as soon as the softmax has read the last S
+            if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+            if (!ok) break;
+            scores(k, j == mine - 1);
+          }
+          if (do_pv) {
+            if (j == 1 && before > 0)
+              ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
+            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+          }
+          if (kTurns && (x > 0 || turns > 0))
+            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+          if (!ok) break;
+          if (do_pv) {
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
+                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv,
+                           (j == 1 && kk == 0) ? 0u : 1u);
+            }
+            __syncwarp();
+            ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+              if (L::kSepP) tc::commit(&B->pv_done[x]);
+              if (j == mine) tc::commit(&B->o_full[x]);
+            }
+            __syncwarp();
+          }
+          if (!L::kSepP && do_s) scores(k, j == mine - 1);
+          if (tc::elect_one()) {
+            if (kTurns) mbar_arrive(&B->turn[x ^ 1]);
+            // a stage is free once the MMAs on it are done (both warps', unless
+            // split)
+            if (use_v) tc::commit(&B->v_empty[sv]);
+            if (use_k) tc::commit(&B->k_empty[sk]);
+          }
+          __syncwarp();
+          issued = true;
+          tiles += do_s;
         }
         c += nt;
         ++segs;
+        items += mine > 0;
       }
       // everything issued above has completed before TMEM is released
       if (issued) {
-        if (tc::elect_one()) tc::commit(&B->done);
+        if (tc::elect_one()) tc::commit(&B->done[x]);
         __syncwarp();
-        mbar_wait(&B->done, 0);
+        mbar_wait(&B->done[x], 0);
       }
-    } else if (warp == kKWarp || warp == kVWarp) {
+    } else if (warp == kKWarp || warp == kVWarp<FP8>) {
       // ---------------------------------------------------------------- loads
-      const bool vop = warp == kVWarp;
-      const int NS = FP8 ? RS : (vop ? VS : KS);
-      uint64_t* full = FP8 ? B->raw_full[vop] : (vop ? B->v_full : B->k_full);
-      uint64_t* empty = FP8 ? B->raw_empty[vop] : (vop ? B->v_empty : B->k_empty);
+      const bool v_only = warp == kVWarp<FP8>;
+      const int NS = FP8 ? RS : (v_only ? VS : KS);
       constexpr int kStage = FP8 ? L::kRaw : L::kOp;
-      uint8_t* ring = smem + (FP8 ? L::kRawOff + (vop ? RS * kStage : 0)
-                                  : (vop ? L::kVOff : L::kKOff));
-      const uint8_t* pool = static_cast<const uint8_t*>(vop ? p.v_pool : p.k_pool);
-      const CUtensorMap* map = vop ? &tmv : &tmk;
-      // K/V are read once, unless by the CTA alongside too
+      // K/V are read once (or twice at about the same time)
       const uint64_t policy = l2_policy_evict_first();
       Reader rd;
       Seg g;
@@ -525,19 +510,24 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           // the next tile's block ids arrive while this tile waits for a stage
           const int id_next = t + 1 < g.t1 ? block_id(p, g, t + 1, lane) : -1;
           const int st = c % NS;
-          const bool w = c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
-          ok = __all_sync(0xffffffffu, w);
-          if (!ok) break;
-          load_tile<D, FP8>(p, g, t, ring + st * kStage, map, pool, &full[st], lane, id, !vop,
-                            policy);
+#pragma unroll 1
+          for (int kv = v_only; kv < (FP8 ? 2 : v_only + 1); ++kv) {  // 0: K, 1: V
+            uint64_t* full = FP8 ? B->raw_full[kv] : (kv ? B->v_full : B->k_full);
+            uint64_t* empty = FP8 ? B->raw_empty[kv] : (kv ? B->v_empty : B->k_empty);
+            uint8_t* ring = smem + (FP8 ? L::kRawOff + kv * RS * kStage
+                                        : (kv ? L::kVOff : L::kKOff));
+            if (c >= (uint32_t)NS) ok = ok && wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+            if (!ok) break;
+            load_tile<D, FP8>(p, g, t, ring + st * kStage, kv ? &tmv : &tmk,
+                              static_cast<const uint8_t*>(kv ? p.v_pool : p.k_pool), &full[st],
+                              lane, id, kv == 0, policy);
+          }
           id = id_next;
-          if (!FP8 && !vop && t == g.t0) {
+          if (!FP8 && !v_only && t == g.t0) {
 #pragma unroll
             for (int x = 0; x < L::kQ; ++x) {
               if (!ok || tile_nodes(g, x) == 0) continue;
-              const bool w =
-                  nq[x] == 0 || wait_ok(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
-              ok = __all_sync(0xffffffffu, w);
+              if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
               if (!ok) continue;
               ++nq[x];
               if (lane == 0) {
@@ -556,12 +546,15 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
       }
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
-        mbar_wait(&full[u % NS], (u / NS) & 1);
+        for (int kv = v_only; kv < (FP8 ? 2 : v_only + 1); ++kv)
+          mbar_wait(FP8 ? &B->raw_full[kv][u % NS]
+                        : (kv ? &B->v_full[u % NS] : &B->k_full[u % NS]),
+                    (u / NS) & 1);
       if (!FP8)
 #pragma unroll
         for (int x = 0; x < L::kQ; ++x)
           if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
-    } else if (warp == kSchedWarp) {
+    } else if (warp == kSchedWarp<FP8>) {
       // ------------------------------------------------------------ scheduler
       int first;
       const Shares sh(total_weight(p, lane, blockIdx.x == 0, first), gridDim.x / nrg);
@@ -620,7 +613,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
         ++k;
         if (g.s < 0) break;
       }
-    } else if (FP8 && warp >= 12) {
+    } else if (FP8 && warp >= kConvWarp) {
       // ------------------------------------- converters: 4 warps for K, 4 for V
       const bool vop = warp >= 16;
       const int ct = threadIdx.x - (vop ? 512 : 384);  // 0 .. 127
@@ -779,7 +772,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
           if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
-          l += attn::tile_weights<kOpBf16, 0>(s, 0, sle, neg_m, pk);
+          l += attn::tile_weights<kOpBf16>(s, 0, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
             ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
@@ -794,7 +787,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
             tc::fence_before();
             mbar_arrive(&B->s_empty[x]);
           }
-          l += attn::tile_weights<kOpBf16, 0>(s, FP8 ? 0 : 1, sle, neg_m, pk);
+          l += attn::tile_weights<kOpBf16>(s, FP8 ? 0 : 1, sle, neg_m, pk);
           tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();
