@@ -333,22 +333,25 @@ pa_status pa_alloc_truncate(pa_alloc* a, int64_t seq, int n_tokens, const int32_
   for (size_t i = first; i < n && i < s.tokens.size(); i++)
     if (tokens[i - first] != s.tokens[i]) return PA_ERR_INVALID_ARG;
   const bool more = first <= s.tokens.size() && s.tokens.size() < n;
-  try {  // whatever can fail, before anything changes
+  try {
+    // what can fail comes before anything changes, but for the nodes of the
+    // free lists
     if (more) s.tokens.reserve(n);
+    s.hchain.reserve(n / kB);
+    if (more) s.tokens.insert(s.tokens.end(), tokens + (s.tokens.size() - first), tokens + n_ids);
+    if (s.tokens.size() > n) s.tokens.resize(n);
+    if (s.hchain.size() > n / kB) s.hchain.resize(n / kB);
+    s.n_tokens = n_tokens;
+    s.known = s.tokens.size() == n;
+    const size_t keep = (n + kB - 1) / kB;
+    while (s.blocks.size() > keep) {  // last block first
+      a->release(s.blocks.back());
+      s.blocks.pop_back();
+    }
+    a->register_full(s, 0);
   } catch (...) {
     return PA_ERR_OOM;
   }
-  if (more) s.tokens.insert(s.tokens.end(), tokens + (s.tokens.size() - first), tokens + n_ids);
-  if (s.tokens.size() > n) s.tokens.resize(n);
-  if (s.hchain.size() > n / kB) s.hchain.resize(n / kB);
-  const size_t keep = (n + kB - 1) / kB;
-  while (s.blocks.size() > keep) {  // last block first
-    a->release(s.blocks.back());
-    s.blocks.pop_back();
-  }
-  s.n_tokens = n_tokens;
-  s.known = s.tokens.size() == n;
-  a->register_full(s, 0);
   return PA_OK;
 }
 

@@ -761,7 +761,7 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
     // operands widen exactly there, so V needs no 2^-8 fold
     const uint64_t rows = (uint64_t)n_chunks * n_kv_heads * p.stage_rows;
     if (rows >= (uint64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
-    p.out_mul = fp8 ? v_scale * kFp8VUnscale : 1.f;
+    p.out_mul = fp8 ? v_scale : 1.f;
     const uint16_t* kst = static_cast<const uint16_t*>(workspace);
     if (!get_map(kst, rows, 128, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &tmk) ||
         !get_map(kst + rows * 128, rows, 128, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &tmv))

@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++n_mine;
       const bool valid = qi < it.len;
-      const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+      const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
       T16* out = static_cast<T16*>(p.out) +
                  ((size_t)(it.start + qi) * p.n_q + it.h0 + (r & ((1 << lhb) - 1))) * D;
       if (!valid) out = nullptr;

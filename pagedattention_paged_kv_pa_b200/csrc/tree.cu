@@ -830,9 +830,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
         if (!ok) break;
         const float2 a = red[0], b = red[128];
         m = fmaxf(a.x, b.x);
-        w0 = a.x == -INFINITY ? 0.f : exp2f(a.x - m);
-        w1 = b.x == -INFINITY ? 0.f : exp2f(b.x - m);
-        l = w0 * a.y + w1 * b.y;
+        // (a sum that is not finite stays so)
+        w0 = m == -INFINITY ? 0.f : exp2f(a.x - m);
+        w1 = m == -INFINITY ? 0.f : exp2f(b.x - m);
+        l = m == -INFINITY ? a.y + b.y : w0 * a.y + w1 * b.y;
       } else if (m == -INFINITY) {
         w0 = 0.f;
       }
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
                                      : ((size_t)blockIdx.x * 2 + g.slot) * (SPLIT ? 128 : 256) +
                                            (SPLIT ? 0 : x * 128) + r;
       if (g.slot < 0) {
-        const float inv = l > 0.f ? p.out_mul / l : 0.f;
+        const float inv = l == 0.f ? 0.f : p.out_mul / l;
         w0 *= inv;
         w1 *= inv;
       } else if (valid && (!SPLIT || x == 0)) {
@@ -939,7 +940,10 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
     const int k = min(32, last - c0 + 1);
     const float2 v = lane < k ? p.ws_ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.f);
     const float mn = fmaxf(M, warp_max_xor(v.x, 1));
-    if (mn == -INFINITY) continue;
+    if (mn == -INFINITY) {  // nothing seen, unless a sum is not a number
+      if (__any_sync(0xffffffffu, v.y != 0.f)) Ls = NAN;
+      continue;
+    }
     const float old = exp2f(M - mn), w = exp2f(v.x - mn);
     M = mn;
     Ls *= old;
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
       for (int e = 0; e < V; ++e) acc[e] += wi == 0.f ? 0.f : wi * o[e];
     }
   }
-  const float inv = Ls > 0.f ? p.out_mul / Ls : 0.f;
+  const float inv = Ls == 0.f ? 0.f : p.out_mul / Ls;
   constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
   uint32_t* out = reinterpret_cast<uint32_t*>(
       static_cast<OutT*>(p.out) +

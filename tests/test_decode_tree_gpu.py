@@ -260,3 +260,69 @@ def test_repeats_are_bit_equal(B, cuda_device):
     a = c.run(B)
     for _ in range(3):
         assert torch.equal(a, c.run(B))
+
+
+@pytest.mark.parametrize("dt,fp8", TYPES)
+@pytest.mark.parametrize("G", [5, 6])
+@pytest.mark.parametrize("nodes", [25, 64])
+def test_groups_that_leave_rows_of_a_tile_empty(B, cuda_device, dt, fp8, G, nodes):
+    c = Case([nodes, 500, 131], nodes, G, 1, 128, dt, fp8, cuda_device,
+             lens=[nodes, nodes - 3, 1], seed=G)
+    c.check(c.run(B), f"G={G} nodes={nodes} {dt} fp8={fp8}")
+
+
+@pytest.mark.parametrize("nodes", [6, 40])
+def test_a_bad_key_reaches_only_the_rows_that_see_it(B, cuda_device, nodes):
+    c = Case([400, 350], nodes, 8, 2, 128, torch.bfloat16, False, cuda_device, seed=16)
+    bad = nodes // 2  # a node of sequence 0
+    at = 400 - nodes + bad
+    good = c.k.clone()
+    c.k[c.tables[0, at // 16].item(), :, at % 16] = float("nan")
+    out = c.run(B)
+    c.k = good
+    sees = (c.masks[0] >> bad & 1).bool().to(c.dev)
+    assert sees.any() and torch.isnan(out[0][sees]).all()
+    out[0][sees] = 0
+    full = c.run(B)
+    full[0][sees] = 0
+    c.check(out, "the other sequence", seqs=[1])
+    assert torch.equal(out[0], full[0])
+
+
+@pytest.mark.parametrize("nodes", [3, 17, 64])
+def test_the_workspace_size_holds(B, cuda_device, nodes):
+    c = Case([3000, 1500, 40, 2200], nodes, 16, 2, 128, torch.bfloat16, False, cuda_device, seed=17)
+    n = B.pa_decode_tree_workspace_size(4, nodes, 16, 2, 128)
+    room = torch.full((n + 8192,), 0x5a, dtype=torch.uint8, device=cuda_device)
+    out = c.run(B, workspace=room[4096:4096 + n])
+    assert (room[:4096] == 0x5a).all() and (room[-4096:] == 0x5a).all()
+    c.check(out, f"{nodes} nodes")
+    with pytest.raises(B.PAError):
+        c.run(B, workspace=room[4096:4096 + n - 16])
+
+
+def test_captured_graphs_with_a_workspace_each(B, cuda_device):
+    cs = [Case([2500, 700], 12, 16, 2, 128, torch.bfloat16, False, cuda_device, seed=40 + i)
+          for i in range(2)]
+    outs = [torch.zeros_like(c.q) for c in cs]
+    ws = [B.alloc_tree_workspace(c.q, c.k) for c in cs]
+    args = [c.args() for c in cs]
+    graphs = []
+    for (a, k), o, w in zip(args, outs, ws):
+        B.pa_decode_tree(o, *a, **k, workspace=w)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.pa_decode_tree(o, *a, **k, workspace=w)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for i, (c, o) in enumerate(zip(cs, outs)):
+        c.check(o, f"graph {i}")

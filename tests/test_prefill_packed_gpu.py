@@ -194,3 +194,39 @@ def test_repeats_are_bit_equal(B, cuda_device):
     for _ in range(3):
         b, _ = run(B, q, k, v, start, 0.09)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_bad_key_reaches_only_the_rows_that_see_it(B, cuda_device, d):
+    n, at = 300, 140
+    q, k, v, start = make([n], 4, 2, d, torch.bfloat16, cuda_device, seed=12)
+    k[at] = float("nan")
+    out, err = run(B, q, k, v, start, 0.09)
+    assert err == 0
+    assert torch.isnan(out[at:]).all()
+    ref, mag = plain64.attend(q[:at], k[:at], v[:at], plain64.causal(at, q.device), 0.09)
+    plain64.check(out[:at], ref, mag, at, v[:at].abs().max().item(), q.dtype, "before the bad key")
+
+
+def test_strides_of_different_tensors(B, cuda_device):
+    # q, k and v with their own strides, wider than a token
+    g = torch.Generator(device=cuda_device).manual_seed(13)
+    n, n_q, n_kv, d = 210, 6, 2, 64
+    base = [torch.randn(n, w, d, device=cuda_device, generator=g, dtype=torch.float16)
+            for w in (n_q + 5, n_kv + 1, n_kv + 9)]
+    q, k, v = base[0][:, 2:2 + n_q], base[1][:, 1:], base[2][:, 3:3 + n_kv]
+    start = torch.tensor([0, 150, 210], dtype=torch.int32, device=cuda_device)
+    out, err = run(B, q, k, v, start, 0.125)
+    assert err == 0
+    check(out, q, k, v, [150, 60], 0.125, "strided")
+
+
+def test_nothing_is_written_around_the_output(B, cuda_device):
+    lens, n_q, d = [129, 31], 5, 128
+    q, k, v, start = make(lens, n_q, 1, d, torch.bfloat16, cuda_device, seed=14)
+    room = torch.full((160 * n_q * d + 4096,), 3.0, device=cuda_device, dtype=torch.bfloat16)
+    out = room[2048:-2048].view(160, n_q, d)
+    B.pa_prefill_packed(out, q, k, v, start, 0.09)
+    torch.cuda.synchronize()
+    assert (room[:2048] == 3).all() and (room[-2048:] == 3).all()
+    check(out, q, k, v, lens, 0.09, "inside a larger buffer")
