@@ -736,9 +736,11 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
           tc::fence_after();
           const int key = (g.t0 + ti) * kTileN;
           const bool full = key + kTileN <= P && p.scale_log2 > 0.f;
-          uint32_t vis[4];
+          uint32_t vis[4] = {};
+          if (!full) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) vis[w] = seen_bits(key + 32 * w, P, mask);
+            for (int w = 0; w < 4; ++w) vis[w] = seen_bits(key + 32 * w, P, mask);
+          }
           float s[FP8 ? 64 : kTileN];
           float mx, sle = FP8 && !full ? 1.f : sl;
           if constexpr (FP8) {
