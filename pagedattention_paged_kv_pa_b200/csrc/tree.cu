@@ -28,16 +28,15 @@
 // tree_merge_kernel, a programmatic dependent, combines in share order.
 //
 // Roles: warps 0-3 softmax of A, 4-7 of B (one thread per row), warps 8 and 9
-// issue the MMAs of A and B, warp 10 loads Q and K, warp 11 V (16-token blocks
-// by TMA through the block table; rows of the block a context ends in are
-// copied, rows past it and blocks with a bad id zeroed by the warp itself),
-// warp 12 walks the share.  E4M3 caches: warp 10 brings raw rows of K and V into
-// rings of raw tiles, warp 11 walks the share, warps 12-15 widen K and 16-19 V
-// to the f16 operands (code x 2^-8, exact, undone by the score and output
-// scales); the K converters also write the query rows, scaled by a power of two
-// into f16's range when they are bf16, and P is f16.  Every wait is bounded; a
-// role that gives up flags PA_DEVERR_TIMEOUT and leaves, and the CTA drains its
-// loads and MMAs and frees TMEM.
+// issue the MMAs of A and B, warps 10 and 11 load K (and Q), 12 and 13 V (16-token
+// blocks by TMA through the block table; rows of the block a context ends in
+// are copied, rows past it and blocks with a bad id zeroed by the warp itself),
+// warp 14 walks the share.  E4M3 caches: K and V arrive as raw tiles, and warps
+// 16-19 widen K, 20-23 V to the f16 operands (code x 2^-8, exact, undone by the
+// score and output scales); the K converters also write the query rows, scaled
+// by a power of two into f16's range when they are bf16, and P is f16.  Every
+// wait is bounded; a role that gives up flags PA_DEVERR_TIMEOUT and leaves, and
+// the CTA drains its loads and MMAs and frees TMEM.
 #include <type_traits>
 
 #include "attn_tile.cuh"
@@ -50,13 +49,8 @@ namespace {
 using attn::kTileM;
 using attn::kTileN;
 
-// 16-bit caches have a load warp each for K and V (and three idle warps), E4M3
-// caches one for both and the converters
-constexpr int kMmaWarp = 8, kKWarp = 10, kConvWarp = 12;
-template <bool FP8>
-constexpr int kVWarp = FP8 ? -1 : 11;
-template <bool FP8>
-constexpr int kSchedWarp = FP8 ? 11 : 12;
+// two load warps each for K (10, 11) and V (12, 13)
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 14, kConvWarp = 16;  // 15 idle
 constexpr int kSegs = 4;  // segments scheduled ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMergeRows = 16;  // rows of a merge CTA
@@ -67,8 +61,12 @@ struct Lay {
   static constexpr int kRaw = kTileN * D;     // one E4M3 K or V tile
   static constexpr int kQ = SPLIT ? 1 : 2;    // Q tiles
   static constexpr int kScale = 128 / D;
-  static constexpr int kKS = (FP8 ? 2 : 3) * kScale;
-  static constexpr int kVS = (FP8 ? (SPLIT || D == 64 ? 2 : 1) : (SPLIT ? 3 : 2)) * kScale;
+  // K and V stages.  Split: even numbers, so that a stage always belongs to the
+  // same tile X (a segment takes an even number of stages, the last one empty
+  // if need be) and X's MMA warp sees every phase of its stages' barriers
+  static constexpr int kKS = (FP8 ? 2 : (SPLIT ? 4 : 3)) * kScale;
+  static constexpr int kVS = (FP8 && !SPLIT && D == 128 ? 1 : 2) * kScale;
+  static_assert(!SPLIT || (kKS % 2 == 0 && kVS % 2 == 0), "a stage per tile");
   static constexpr int kRS = FP8 ? 2 * kScale : 0;  // raw K stages, and raw V stages
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kQ * kOp;
@@ -84,12 +82,12 @@ struct Lay {
   static constexpr bool kSepP = D == 64;
   static constexpr int tP(int x) { return kSepP ? 256 + 64 * x : 128 * x; }
   static constexpr int tO(int x) { return kSepP ? 384 + 64 * x : 256 + 128 * x; }
-  static constexpr int kThreads = FP8 ? 640 : 512;
-  // registers: 640 x 96 = 61,440 = 256 x 128 + 384 x 72 + 1,024, or 512 x 128 =
-  // 65,536 = 256 x 184 + 256 x 72
-  static constexpr int kSoftRegs = FP8 ? 128 : 184, kOtherRegs = FP8 ? 72 : 72;
-  // readers of a segment: 8 softmax warps, 2 MMA, 2 loads or 1 and 8 converters
-  static constexpr uint32_t kReaders = FP8 ? 19 : 12;
+  static constexpr int kThreads = FP8 ? 768 : 512;
+  // registers: 768 x 80 = 61,440 = 256 x 128 + 512 x 56, or 512 x 128 = 65,536 =
+  // 256 x 184 + 256 x 72
+  static constexpr int kSoftRegs = FP8 ? 128 : 184, kOtherRegs = FP8 ? 56 : 72;
+  // readers of a segment: 8 softmax warps, 2 MMA, 4 loads, 8 converters
+  static constexpr uint32_t kReaders = FP8 ? 22 : 14;
 };
 
 struct Seg {
@@ -100,7 +98,7 @@ struct Seg {
 };
 
 struct Bars {
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], raw_full[2][4], raw_empty[2][4];
+  uint64_t k_full[8], k_empty[8], v_full[4], v_empty[4], raw_full[2][4], raw_empty[2][4];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], red[2];
   uint64_t s_empty[2], pv_done[2];  // P beside S only
@@ -218,30 +216,31 @@ __device__ __forceinline__ uint32_t raw_off(int row, int chunk) {
   return D == 128 ? swz128(row * 128 + chunk * 16) : swz64(row * 64 + chunk * 16);
 }
 
-// The block id of lane m < 8's block m of tile t (-1 past the context).
-__device__ __forceinline__ int block_id(const TreeParams& p, const Seg& g, int t, int lane) {
-  const int blk = t * 8 + lane;
-  return lane < 8 && blk * 16 < g.ctx ? __ldg(&p.block_tables[(size_t)g.s * p.max_blocks + blk])
+// The block id of lane m < 4's block 4 half + m of tile t (-1 past the context).
+__device__ __forceinline__ int block_id(const TreeParams& p, const Seg& g, int t, int half,
+                                        int lane) {
+  const int blk = t * 8 + half * 4 + lane;
+  return lane < 4 && blk * 16 < g.ctx ? __ldg(&p.block_tables[(size_t)g.s * p.max_blocks + blk])
                                       : -1;
 }
 
-// Loads tile t of a (sequence, kv head) into `dst`, by one warp: whole blocks
-// of the context by TMA, the other rows written here.
+// Loads half of tile t of a (sequence, kv head) into `dst`, by one warp: whole
+// blocks of the context by TMA, the other rows written here.
 template <int D, bool FP8>
-__device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int t, uint8_t* dst,
+__device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int t, int half, uint8_t* dst,
                                           const CUtensorMap* map, const uint8_t* pool,
                                           uint64_t* full, int lane, int phys, bool report,
                                           uint64_t policy) {
   constexpr int kRow = FP8 ? D : 2 * D;  // bytes of a row
-  const int blk = t * 8 + lane;
-  const bool in_ctx = lane < 8 && blk * 16 < g.ctx;
+  const int b = half * 4 + lane, blk = t * 8 + b;
+  const bool in_ctx = lane < 4 && blk * 16 < g.ctx;
   const bool in_range = phys >= 0 && phys < p.num_blocks;
   if (report && in_ctx && !in_range) flag_error(p.dev_err, PA_DEVERR_BLOCK_ID);
   const bool whole = in_ctx && in_range && blk * 16 + 16 <= g.ctx;
   const uint32_t whole_m = __ballot_sync(0xffffffffu, whole);
-  for (uint32_t pm = __ballot_sync(0xffffffffu, lane < 8 && !whole); pm; pm &= pm - 1) {
-    const int m = __ffs(pm) - 1;
-    const int ph = __shfl_sync(0xffffffffu, phys, m);
+  for (uint32_t pm = __ballot_sync(0xffffffffu, lane < 4 && !whole); pm; pm &= pm - 1) {
+    const int ph = __shfl_sync(0xffffffffu, phys, __ffs(pm) - 1);
+    const int m = half * 4 + __ffs(pm) - 1;  // block of the tile
     const bool ok_id = ph >= 0 && ph < p.num_blocks;
     const int nvalid = ok_id ? max(0, min(16, g.ctx - (t * 8 + m) * 16)) : 0;
     const uint8_t* src = pool + (long long)(ok_id ? ph * p.n_kv + g.h : 0) * 16 * kRow;
@@ -261,11 +260,11 @@ __device__ __forceinline__ void load_tile(const TreeParams& p, const Seg& g, int
   if (whole) {
     const int y = (phys * p.n_kv + g.h) * 16;  // row of the [rows][D] view
     if constexpr (FP8) {
-      tma_load_2d_hint(dst + lane * 16 * kRow, map, full, 0, y, policy);
+      tma_load_2d_hint(dst + b * 16 * kRow, map, full, 0, y, policy);
     } else {
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        tma_load_2d_hint(dst + h * 16384 + lane * 2048, map, full, 64 * h, y, policy);
+        tma_load_2d_hint(dst + h * 16384 + b * 2048, map, full, 64 * h, y, policy);
     }
   }
 }
@@ -310,7 +309,7 @@ __device__ __forceinline__ uint32_t seen_bits(int first, int P, uint64_t mask) {
 }
 
 template <bool BF16, int D, bool FP8, bool SPLIT>
-__global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
+__global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
     tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -331,16 +330,16 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
-      mbar_init(&B->k_full[s], FP8 ? 128 : 1);
+      mbar_init(&B->k_full[s], FP8 ? 128 : 2);
       mbar_init(&B->k_empty[s], SPLIT ? 1 : 2);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(&B->v_full[s], FP8 ? 128 : 1);
+      mbar_init(&B->v_full[s], FP8 ? 128 : 2);
       mbar_init(&B->v_empty[s], SPLIT ? 1 : 2);
     }
     for (int s = 0; s < RS; ++s) {
       for (int v = 0; v < 2; ++v) {
-        mbar_init(&B->raw_full[v][s], 1);
+        mbar_init(&B->raw_full[v][s], 2);
         mbar_init(&B->raw_empty[v][s], 128);
       }
     }
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tc::alloc(&B->tmem_base, kTmemCols);
-  if (warp == kKWarp && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     if (!FP8) prefetch_tensormap(&tmq);
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
@@ -426,9 +425,10 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
         const uint32_t before = SPLIT ? segs : items;  // O_X read out so often
         for (int j = 0; j <= n && ok; ++j, ++turns) {
           const bool do_pv = j > 0 && j <= mine, do_s = j < mine;
-          // split: own key tiles; else A's and B's, a tile of no rows included
+          // split: every second key tile (and stage); else all of them, with
+          // rows or without
           const uint32_t ck = c + (SPLIT ? 2 * j + x : j), cv = ck - (SPLIT ? 2 : 1);
-          const bool use_k = SPLIT ? do_s : j < n, use_v = SPLIT ? do_pv : j > 0;
+          const bool use_k = j < n, use_v = j > 0;
           const int sk = ck % KS, sv = cv % VS;
           const uint64_t v = dV + sv * kOpStep, k = dK + sk * kOpStep;
           const uint32_t par = (tiles - 1) & 1;
@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
             scores(k, j == mine - 1);
           }
           if (do_pv) {
+            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
             if (j == 1 && before > 0)
               ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
-            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
           }
           if (kTurns && (x > 0 || turns > 0))
             ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
           issued = true;
           tiles += do_s;
         }
-        c += nt;
+        c += SPLIT ? 2 * n : nt;
         ++segs;
         items += mine > 0;
       }
@@ -490,13 +490,23 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
         __syncwarp();
         mbar_wait(&B->done[x], 0);
       }
-    } else if (warp == kKWarp || warp == kVWarp<FP8>) {
+    } else if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
       // ---------------------------------------------------------------- loads
-      const bool v_only = warp == kVWarp<FP8>;
-      const int NS = FP8 ? RS : (v_only ? VS : KS);
+      // two warps for K, two for V: each loads half the blocks of every tile
+      // (a copy takes a lane of a warp about 100 clocks to issue)
+      const bool vop = warp >= kLoadWarp + 2;
+      const int half = (warp - kLoadWarp) & 1;
+      const int NS = FP8 ? RS : (vop ? VS : KS);
+      uint64_t* full = FP8 ? B->raw_full[vop] : (vop ? B->v_full : B->k_full);
+      uint64_t* empty = FP8 ? B->raw_empty[vop] : (vop ? B->v_empty : B->k_empty);
       constexpr int kStage = FP8 ? L::kRaw : L::kOp;
+      uint8_t* ring = smem + (FP8 ? L::kRawOff + (vop ? RS * kStage : 0)
+                                  : (vop ? L::kVOff : L::kKOff));
+      const uint8_t* pool = static_cast<const uint8_t*>(vop ? p.v_pool : p.k_pool);
+      const CUtensorMap* map = vop ? &tmv : &tmk;
       // K/V are read once (or twice at about the same time)
       const uint64_t policy = l2_policy_evict_first();
+      const bool q_too = !FP8 && warp == kLoadWarp;  // the first one loads Q
       Reader rd;
       Seg g;
       bool ok = true;
@@ -505,25 +515,24 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
-        int id = block_id(p, g, g.t0, lane);
+        int id = block_id(p, g, g.t0, half, lane);
         for (int t = g.t0; t < g.t1 && ok; ++t, ++c) {
           // the next tile's block ids arrive while this tile waits for a stage
-          const int id_next = t + 1 < g.t1 ? block_id(p, g, t + 1, lane) : -1;
+          const int id_next = t + 1 < g.t1 ? block_id(p, g, t + 1, half, lane) : -1;
           const int st = c % NS;
-#pragma unroll 1
-          for (int kv = v_only; kv < (FP8 ? 2 : v_only + 1); ++kv) {  // 0: K, 1: V
-            uint64_t* full = FP8 ? B->raw_full[kv] : (kv ? B->v_full : B->k_full);
-            uint64_t* empty = FP8 ? B->raw_empty[kv] : (kv ? B->v_empty : B->k_empty);
-            uint8_t* ring = smem + (FP8 ? L::kRawOff + kv * RS * kStage
-                                        : (kv ? L::kVOff : L::kKOff));
-            if (c >= (uint32_t)NS) ok = ok && wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
-            if (!ok) break;
-            load_tile<D, FP8>(p, g, t, ring + st * kStage, kv ? &tmv : &tmk,
-                              static_cast<const uint8_t*>(kv ? p.v_pool : p.k_pool), &full[st],
-                              lane, id, kv == 0, policy);
-          }
+          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+          if (!ok) break;
+          load_tile<D, FP8>(p, g, t, half, ring + st * kStage, map, pool, &full[st], lane, id,
+                            !vop, policy);
           id = id_next;
-          if (!FP8 && !v_only && t == g.t0) {
+          if (SPLIT && !FP8 && t + 1 == g.t1 && ((g.t1 - g.t0) & 1)) {  // B's empty stage
+            ++c;
+            const int se = c % NS;
+            if (c >= (uint32_t)NS) ok = wait_all(&empty[se], (c / NS - 1) & 1, B, p.dev_err);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&full[se]);
+          }
+          if (q_too && t == g.t0) {
 #pragma unroll
             for (int x = 0; x < L::kQ; ++x) {
               if (!ok || tile_nodes(g, x) == 0) continue;
@@ -546,15 +555,12 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       }
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
-        for (int kv = v_only; kv < (FP8 ? 2 : v_only + 1); ++kv)
-          mbar_wait(FP8 ? &B->raw_full[kv][u % NS]
-                        : (kv ? &B->v_full[u % NS] : &B->k_full[u % NS]),
-                    (u / NS) & 1);
-      if (!FP8)
+        mbar_wait(&full[u % NS], (u / NS) & 1);
+      if (q_too)
 #pragma unroll
         for (int x = 0; x < L::kQ; ++x)
           if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
-    } else if (warp == kSchedWarp<FP8>) {
+    } else if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
       int first;
       const Shares sh(total_weight(p, lane, blockIdx.x == 0, first), gridDim.x / nrg);
@@ -615,8 +621,8 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       }
     } else if (FP8 && warp >= kConvWarp) {
       // ------------------------------------- converters: 4 warps for K, 4 for V
-      const bool vop = warp >= 16;
-      const int ct = threadIdx.x - (vop ? 512 : 384);  // 0 .. 127
+      const bool vop = warp >= kConvWarp + 4;
+      const int ct = (threadIdx.x - 32 * kConvWarp) & 127;
       const int NS = vop ? VS : KS;
       uint64_t* full = vop ? B->v_full : B->k_full;
       uint64_t* empty = vop ? B->v_empty : B->k_empty;
@@ -624,7 +630,7 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       Reader rd;
       Seg g;
       bool ok = true;
-      uint32_t c = 0;
+      uint32_t c = 0, cr = 0;  // operand tiles, raw tiles
       int nq[2] = {0, 0};
       while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
         __syncwarp();
@@ -634,10 +640,9 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
         for (int x = 0; x < L::kQ; ++x) {
           const int nodes = tile_nodes(g, x);
           if (vop || !ok || nodes == 0) continue;
-          // the rows of the segment before are done with, and the exponents of
-          // the one before that
+          // S of the segment before is done: its rows are done with, and the
+          // exponents of the one before that have been read (its P was written)
           if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
-          if (nq[x] > 1) ok = ok && wait_all(&B->o_free[x], nq[x] & 1, B, p.dev_err);
           if (!ok) continue;
           const int ri = ct / G, node = (SPLIT ? 0 : 2 * rg + x) * QT + ri;
           write_query_row<BF16, D>(
@@ -650,9 +655,9 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
           mbar_arrive(&B->q_full[x]);
           ++nq[x];
         }
-        for (int t = g.t0; t < g.t1 && ok; ++t, ++c) {
-          const int st = c % NS, rs = c % RS;
-          bool w = wait_ok(&B->raw_full[vop][rs], (c / RS) & 1, B, p.dev_err);
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++c, ++cr) {
+          const int st = c % NS, rs = cr % RS;
+          bool w = wait_ok(&B->raw_full[vop][rs], (cr / RS) & 1, B, p.dev_err);
           w = w && (c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err));
           ok = __all_sync(0xffffffffu, w);
           if (!ok) break;
@@ -680,6 +685,12 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
           mbar_arrive(&B->raw_empty[vop][rs]);
           tc::fence_async_smem();
           mbar_arrive(&full[st]);
+        }
+        if (SPLIT && ok && ((g.t1 - g.t0) & 1)) {  // B's empty stage
+          const int st = c % NS;
+          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+          if (ok) mbar_arrive(&full[st]);
+          ++c;
         }
       }
     }
@@ -719,12 +730,6 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       uint64_t mask = valid ? __ldg(&p.masks[(size_t)g.s * p.q_len + node]) : 0ull;
       if (g.n < 64) mask &= (1ull << g.n) - 1ull;
       float sl = p.scale_log2;
-      if constexpr (FP8) {  // the row went in times 2^e
-        ok = wait_all(&B->q_full[SPLIT ? 0 : x], seg & 1, B, p.dev_err);
-        if (!ok) break;
-        sl *= exp2i(-reinterpret_cast<int8_t*>(
-            smem + L::kExpOff)[((seg & 1) * L::kQ + (SPLIT ? 0 : x)) * 128 + r]);
-      }
       const int P = g.ctx - g.n;  // keys before the tree; may be negative
       float m = -INFINITY, l = 0.f;
       const int nt = g.t1 - g.t0;
@@ -732,6 +737,9 @@ __global__ void __launch_bounds__(FP8 ? 640 : 512, 1)
       for (int ti = SPLIT ? x : 0; ti < nt; ti += SPLIT ? 2 : 1, ++t) {
         ok = wait_all(&B->s_full[x], t & 1, B, p.dev_err);
         if (!ok) break;
+        if (FP8 && !any)  // the row went in times 2^e
+          sl *= exp2i(-reinterpret_cast<int8_t*>(
+              smem + L::kExpOff)[((seg & 1) * L::kQ + (SPLIT ? 0 : x)) * 128 + r]);
         if (live) {  // rows without a node: nothing reads their P or O
           tc::fence_after();
           const int key = (g.t0 + ti) * kTileN;
