@@ -225,7 +225,15 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
  * Supported as pa_decode (head_dim 64 or 128, group size <= 8, 16-bit caches
  * of the query's type and fp8 caches) except q_dtype PA_F32
  * (PA_ERR_UNSUPPORTED).  A block id outside [0, num_blocks) is flagged with
- * PA_DEVERR_BLOCK_ID and its keys read as zeros.
+ * PA_DEVERR_BLOCK_ID and its keys read as zeros.  A context beyond the table is
+ * cut to it and flagged with PA_DEVERR_BLOCK_ID.
+ *
+ * Both products accumulate in fp32.  The softmax weights enter the second one
+ * in the cache's type, or f16 over an fp8 cache (their sum is taken in fp32,
+ * before that rounding).  Keys and values inside a context are read for every
+ * node: a K that is not finite reaches the rows that see it, a V that is not
+ * all rows of its sequence, also those that mask it.  An fp8 cache's NaN codes
+ * read as +-480.  Results do not depend on the order in which CTAs run.
  */
 size_t pa_decode_tree_workspace_size(int num_seqs, int q_len, int n_q_heads, int n_kv_heads,
                                      int head_dim);
@@ -458,8 +466,10 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  * n_q_heads % n_kv_heads == 0.  Pointers must be 16-byte aligned.  Both
  * products accumulate in fp32; the softmax weights enter the second one in
  * `dtype` (their sum is taken in fp32, before that rounding).  No workspace.
- * K and V must be finite within a sequence: a V value that is not reaches the
- * rows that share its 128-key tile, also those before it.
+ * A K that is not finite reaches the rows that see it; a V that is not also
+ * the rows before it that share its 128-key tile.
+ * PA_ERR_UNSUPPORTED as well when (total_tokens / 16 + num_seqs) x n_q_heads
+ * reaches 2^31, num_seqs exceeds 2^20 or n_q_heads 65535.
  */
 pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
                             const int32_t* query_start_loc, float scale, int n_q_heads,
