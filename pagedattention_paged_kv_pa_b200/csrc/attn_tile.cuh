@@ -162,18 +162,18 @@ __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
   tc::wait_st();
 }
 
-// Weights 2^(x sl - m) of keys 64 h .. 64 h + 63 into pk as 16-bit pairs; returns
+// Weights 2^(x sl - m) of keys K0 .. K0 + NK - 1 into pk as 16-bit pairs; returns
 // their fp32 sum.  Masked scores are -inf, with sl = 1 (tile_max has scaled the
 // others), so that tiles with and without a mask run the same code.
-template <bool BF16>
-__device__ __forceinline__ float tile_weights(const float* x, int h, float sl, float neg_m,
-                                              uint32_t (&pk)[32]) {
+template <bool BF16, int NK>
+__device__ __forceinline__ float tile_weights(const float* x, float sl, float neg_m,
+                                              uint32_t* pk) {
   uint64_t s[2] = {0ull, 0ull};
   const uint64_t nm = f2(neg_m, neg_m), s2 = f2(sl, sl);
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < NK / 2; ++c) {
     float a, b;
-    un2(fma2(f2(x[64 * h + 2 * c], x[64 * h + 2 * c + 1]), s2, nm), a, b);
+    un2(fma2(f2(x[2 * c], x[2 * c + 1]), s2, nm), a, b);
     a = tc::ex2(a);
     b = tc::ex2(b);
     s[c & 1] = add2(s[c & 1], f2(a, b));

@@ -108,6 +108,13 @@ __device__ __forceinline__ int seq_span(const PromptParams& p, int s, int& start
   return a < 0 || b < a ? 0 : max(0, min(b, p.total) - a);
 }
 
+// Of the last key tile of item tile X: how many of its four 32-key parts some
+// row sees.
+__device__ __forceinline__ int last_parts(const Item& it, int x, int QT) {
+  const int keys = min(it.len, it.i0 + (x + 1) * QT);
+  return (((keys - 1) & (kTileN - 1)) >> 5) + 1;
+}
+
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tmq,
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lane issues.  The waits of one warp run while the other's MMAs do; they
     // take turns, so that one's batch is not spread over the other's and the
     // softmax passes of A and B fall into opposite phases.
-    constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, kTileN);
+    constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, 0);  // N by tile
     constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
     constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
     const int x = warp - kMmaWarp;
@@ -183,13 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, issued = false;
     uint32_t c = 0;  // stages used before this tile: K of tile j in c, V in c + 1
     uint32_t items = 0, tiles = 0, turns = 0;
-    auto scores = [&](uint64_t k, bool last) {
+    auto scores = [&](uint64_t k, bool last, int parts) {
       tc::fence_after();
       if (tc::elect_one()) {
+        const uint32_t idesc = idesc_s | (uint32_t)(parts * 4) << 17;  // N = 32 parts
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-          tc::mma(tS, dQ + off, k + off, idesc_s, kk > 0);
+          tc::mma(tS, dQ + off, k + off, idesc, kk > 0);
         }
         tc::commit(&B->s_full[x]);
         if (last) tc::commit(&B->q_empty[x]);
@@ -200,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) rd.done(B);
       __syncwarp();
       const int n = max(it.nkt[0], it.nkt[1]), mine = x ? it.nkt[1] : it.nkt[0];
+      const int ends = last_parts(it, x, QT);  // of the last key tile
       if (mine > 0) ok = wait_all(&B->q_full[x], items & 1, B, p.dev_err);
       for (int j = 0; j <= n && ok; ++j, c += 2, ++turns) {
         const uint32_t cv = c - 1;
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (L::kSepP && do_s) {  // S beside P: as soon as the softmax has read the last S
           if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
           if (!ok) break;
-          scores(k, j == mine - 1);
+          scores(k, j == mine - 1, j == mine - 1 ? ends : 4);
         }
         if (do_pv) {
           if (j == 1 && items > 0)
@@ -223,11 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
         if (!ok) break;
         if (do_pv) {
+          const int nk = j == mine ? 2 * ends : 8;  // 16 keys a step = two 8-row groups of V
           tc::fence_after();
           if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 16 keys a step = two 8-row groups of V
-              tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, (j == 1 && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < nk)
+                tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv,
+                           (j == 1 && kk == 0) ? 0u : 1u);
           }
           __syncwarp();
           ok = wait_all(&B->p_full[x], par, B, p.dev_err);
@@ -236,13 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tc::elect_one()) {
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk)
-              tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
+              if (kk < nk) tc::mma_ts(tO, tP + kk * 8, v + kk * 128, idesc_pv, 1u);
             if (L::kSepP) tc::commit(&B->pv_done[x]);
             if (j == mine) tc::commit(&B->o_full[x]);
           }
           __syncwarp();
         }
-        if (!L::kSepP && do_s) scores(k, j == mine - 1);
+        if (!L::kSepP && do_s) scores(k, j == mine - 1, j == mine - 1 ? ends : 4);
         if (tc::elect_one()) {
           if (!L::kSepP) mbar_arrive(&B->turn[x ^ 1]);
           // a stage is free once both warps' MMAs on it are done
@@ -476,22 +488,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             attn::rescale_o(tO, D, alpha);
           }
           const float neg_m = st.m == -INFINITY ? 0.f : -st.m;
-          uint32_t pk[32];
-          st.l += attn::tile_weights<BF16>(s, 0, sle, neg_m, pk);
-          if (L::kSepP && t > 0) {  // P of the tile before has been read
-            ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
+          uint32_t pk[16];
+          const int parts = j == nkt - 1 ? last_parts(it, x, QT) : 4;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c < parts) {  // no row of the tile sees the rest
+              st.l += attn::tile_weights<BF16, 32>(s + 32 * c, sle, neg_m, pk);
+              if (L::kSepP && c == 0 && t > 0) {  // P of the tile before has been read
+                ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+                if (!ok) break;
+                tc::fence_after();
+              }
+              tc::st32x32b_x16(tP + 16 * c, pk);
+            }
+            if (c & 1) {
+              tc::wait_st();
+              tc::fence_before();
+              mbar_arrive(c == 1 ? &B->p_half[x] : &B->p_full[x]);
+            }
           }
-          tc::st32x32b_x32(tP, pk);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&B->p_half[x]);
-          st.l += attn::tile_weights<BF16>(s, 1, sle, neg_m, pk);
-          tc::st32x32b_x32(tP + 32, pk);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&B->p_full[x]);
+          if (!ok) break;
         } else {
           if (L::kSepP) {
             mbar_arrive(&B->s_empty[x]);

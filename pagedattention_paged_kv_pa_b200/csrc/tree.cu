@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
           if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
-          l += attn::tile_weights<kOpBf16>(s, 0, sle, neg_m, pk);
+          l += attn::tile_weights<kOpBf16, 64>(s, sle, neg_m, pk);
           if (L::kSepP && t > 0) {  // P of the tile before has been read
             ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
             if (!ok) break;
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
             tc::fence_before();
             mbar_arrive(&B->s_empty[x]);
           }
-          l += attn::tile_weights<kOpBf16>(s, FP8 ? 0 : 1, sle, neg_m, pk);
+          l += attn::tile_weights<kOpBf16, 64>(s + (FP8 ? 0 : 64), sle, neg_m, pk);
           tc::st32x32b_x32(tP + 32, pk);
           tc::wait_st();
           tc::fence_before();
