@@ -211,15 +211,16 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
  * context_lens[s] < n_s the first nodes have no position and are seen by
  * nobody.  What lies in the cache past the context is never used.
  *
- *   out, q       device [num_seqs][q_len][n_q_heads][head_dim], dtype q_dtype
+ *   out, q       device [num_seqs][q_len][n_q_heads][head_dim], dtype q_dtype;
+ *                must not overlap
  *   q_len        1 .. 64, the most nodes of a sequence
  *   masks        device uint64 [num_seqs][q_len], 8-byte aligned
  *   tree_lens    device int32 [num_seqs], each in [0, q_len]; NULL: all q_len.
  *                A value outside is clamped and flagged (PA_DEVERR_QUERY_LOC)
  *   workspace    >= pa_decode_tree_workspace_size(num_seqs, q_len, n_q_heads,
- *                n_kv_heads, head_dim) bytes, 16-byte aligned (may be NULL
- *                when that size is 0); scratch, contents on entry ignored;
- *                calls that may overlap need one each
+ *                n_kv_heads, head_dim) bytes (at most 39 MiB; the batch and the
+ *                contexts do not matter), 16-byte aligned; scratch, contents on
+ *                entry ignored; calls that may overlap need one each
  *   other arguments as pa_decode.
  *
  * Supported as pa_decode (head_dim 64 or 128, group size <= 8, 16-bit caches
@@ -452,7 +453,8 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  * sequence (a padded batch) are left as they are, and what q, k and v hold
  * there is not used; sequences may be empty.
  *
- *   out            device [total_tokens][n_q_heads][head_dim], packed
+ *   out            device [total_tokens][n_q_heads][head_dim], packed; must not
+ *                  overlap q, k or v
  *   q, k, v        device, token t at element t * stride: [n_q_heads] resp.
  *                  [n_kv_heads][head_dim] elements, so the parts of one fused
  *                  projection need no copy; strides in elements, multiples of
@@ -469,7 +471,7 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  * A K that is not finite reaches the rows that see it; a V that is not also
  * the rows before it that share its 128-key tile.
  * PA_ERR_UNSUPPORTED as well when (total_tokens / 16 + num_seqs) x n_q_heads
- * reaches 2^31, num_seqs exceeds 2^20 or n_q_heads 65535.
+ * reaches 2^31, or num_seqs or n_q_heads exceeds 65535.
  */
 pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
                             const int32_t* query_start_loc, float scale, int n_q_heads,

@@ -783,7 +783,7 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
   if (n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0) return PA_ERR_INVALID_ARG;
   if (num_seqs < 0 || total_tokens < 0 || !valid_dtype(dtype)) return PA_ERR_INVALID_ARG;
   if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-  if (n_q_heads > 65535 || num_seqs > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (n_q_heads > 65535 || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   if (!(scale == scale)) return PA_ERR_INVALID_ARG;
   // the kernel counts (sequence, 16 queries or more, head) items in 31 bits
   if (((int64_t)total_tokens / 16 + num_seqs + 1) * n_q_heads >= (int64_t(1) << 31))

@@ -44,6 +44,9 @@ def test_packed_prefill_refusals(B):
     assert _packed(B, ks=248) == B.PA_ERR_INVALID_ARG
     assert _packed(B, vs=260) == B.PA_ERR_INVALID_ARG          # not a multiple of 8
     assert _packed(B, ks=1 << 38) == B.PA_ERR_UNSUPPORTED
+    assert _packed(B, ns=65536) == B.PA_ERR_UNSUPPORTED
+    assert _packed(B, nq=65536, nkv=1, d=64, qs=1 << 22) == B.PA_ERR_UNSUPPORTED
+    assert _packed(B, nq=4096, qs=1 << 19, total=1 << 24) == B.PA_ERR_UNSUPPORTED  # too many items
     assert _packed(B, ns=0, q=None) == B.PA_OK
     assert _packed(B, total=0, q=None) == B.PA_OK
 
