@@ -53,7 +53,8 @@ using attn::kTileN;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 14, kConvWarp = 16;  // 15 idle
 constexpr int kSegs = 4;  // segments scheduled ahead
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMergeRows = 16;  // rows of a merge CTA
+// rows and warps of a merge CTA: one wave of CTAs, each of which finds its unit
+constexpr int kMergeRows = 32, kMergeWarps = 16;
 
 template <int D, bool FP8, bool SPLIT>
 struct Lay {
@@ -896,7 +897,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
 // step lies in share c, this CTA merges kMergeRows of the unit's rows, a warp a
 // row, from the shares' slots in order.  Every other row was written whole.
 template <typename OutT, int D, bool SPLIT>
-__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeParams p, int ctas) {
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeParams p, int ctas) {
   __shared__ int sh_s, sh_h, sh_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
@@ -937,44 +938,65 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeP
   if (sh_s < 0) return;
   const int G = p.group, QT = kTileM / G, n = seq_nodes(p, sh_s), last = sh_last;
   constexpr int RW = SPLIT ? 128 : 256, V = D / 32;  // rows of a slot, floats a lane
-  const int row = blockIdx.y * kMergeRows + warp;    // of the CTAs side by side: RW each
-  const int rg = row / RW, in = row % RW, r = in % kTileM;
-  const int node = (row / kTileM) * QT + r / G;
-  if (r / G >= QT || node >= n) return;
-  auto slot = [&](int cc) -> size_t {
-    return ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
-  };
-  float M = -INFINITY, Ls = 0.f, acc[V] = {};
-#pragma unroll 1
-  for (int c0 = c; c0 <= last; c0 += 32) {  // 32 pieces at a time, a lane each
-    const int k = min(32, last - c0 + 1);
-    const float2 v = lane < k ? p.ws_ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.f);
-    const float mn = fmaxf(M, warp_max_xor(v.x, 1));
-    if (mn == -INFINITY) {  // nothing seen, unless a sum is not a number
-      if (__any_sync(0xffffffffu, v.y != 0.f)) Ls = NAN;
-      continue;
-    }
-    const float old = exp2f(M - mn), w = exp2f(v.x - mn);
-    M = mn;
-    Ls *= old;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] *= old;
-#pragma unroll 4
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, v.y, i);
-      const float* o = p.ws_o + slot(c0 + i) * D + lane * V;
-      Ls += wi * li;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += wi == 0.f ? 0.f : wi * o[e];
-    }
-  }
-  const float inv = Ls == 0.f ? 0.f : p.out_mul / Ls;
   constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
-  uint32_t* out = reinterpret_cast<uint32_t*>(
-      static_cast<OutT*>(p.out) +
-      (((size_t)sh_s * p.q_len + node) * p.n_q + sh_h * G + r % G) * D + lane * V);
+#pragma unroll 1
+  for (int k = warp; k < kMergeRows; k += kMergeWarps) {
+    const int row = blockIdx.y * kMergeRows + k;  // of the CTAs side by side: RW each
+    const int rg = row / RW, in = row % RW, r = in % kTileM;
+    const int node = (row / kTileM) * QT + r / G;
+    if (r / G >= QT || node >= n) continue;
+    auto slot = [&](int cc) -> size_t {
+      return ((size_t)(cc * p.row_groups + rg) * 2 + (cc == c ? 1 : 0)) * RW + in;
+    };
+    auto load_piece = [&](int cc, float (&y)[V]) {
+      const float* o = p.ws_o + slot(cc) * D + lane * V;
 #pragma unroll
-  for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf>(acc[e] * inv, acc[e + 1] * inv);
+      for (int e = 0; e < V; ++e) y[e] = o[e];
+    };
+    constexpr int kPre = 4;
+    float M = -INFINITY, Ls = 0.f, acc[V] = {};
+#pragma unroll 1
+    for (int c0 = c; c0 <= last; c0 += 32) {  // 32 pieces at a time, a lane each
+      const int nc = min(32, last - c0 + 1);
+      // the first pieces' rows come with the weights, not after them
+      float pre[kPre][V];
+#pragma unroll
+      for (int i = 0; i < kPre; ++i)
+        if (i < nc) load_piece(c0 + i, pre[i]);
+      const float2 v = lane < nc ? p.ws_ml[slot(c0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float mn = fmaxf(M, warp_max_xor(v.x, 1));
+      if (mn == -INFINITY) {  // nothing seen, unless a sum is not a number
+        if (__any_sync(0xffffffffu, v.y != 0.f)) Ls = NAN;
+        continue;
+      }
+      const float old = exp2f(M - mn), w = exp2f(v.x - mn);
+      M = mn;
+      Ls *= old;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= old;
+      auto add = [&](int i, const float (&y)[V]) {
+        const float wi = __shfl_sync(0xffffffffu, w, i), li = __shfl_sync(0xffffffffu, v.y, i);
+        Ls += wi * li;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += wi == 0.f ? 0.f : wi * y[e];
+      };
+#pragma unroll
+      for (int i = 0; i < kPre; ++i)
+        if (i < nc) add(i, pre[i]);
+#pragma unroll 1
+      for (int i = kPre; i < nc; ++i) {
+        float y[V];
+        load_piece(c0 + i, y);
+        add(i, y);
+      }
+    }
+    const float inv = Ls == 0.f ? 0.f : p.out_mul / Ls;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        static_cast<OutT*>(p.out) +
+        (((size_t)sh_s * p.q_len + node) * p.n_q + sh_h * G + r % G) * D + lane * V);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf>(acc[e] * inv, acc[e + 1] * inv);
+  }
 }
 
 template <bool BF16, int D, bool FP8, bool SPLIT>
@@ -994,7 +1016,7 @@ cudaError_t launch_t(const TreeParams& p, const CUtensorMap* tmq, const CUtensor
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)shares, (SPLIT ? 128 : 256) / kMergeRows * p.row_groups);
-  cfg.blockDim = dim3(32 * kMergeRows);
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1031,7 +1053,9 @@ cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspa
   p.row_groups = tiles > 2 ? 2 : 1;
   p.step_keys = tiles == 1 ? 2 * kTileN : kTileN;
   p.log2_step = tiles == 1 ? 8 : 7;
-  p.seg_cost = fp8 ? 2 : 1;
+  // measured, against the time of a step: 1.6 (16-bit, 128 wide), 1.0 (64
+  // wide), 1.5 (E4M3), 1.5 (a step of one tile)
+  p.seg_cost = tiles == 1 && !fp8 && D == 64 ? 1 : 2;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (size_t)kTreeCtas * 2 * (tiles == 1 ? 128 : 256) * D);
   if (D == 128)
