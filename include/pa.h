@@ -470,8 +470,8 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  * `dtype` (their sum is taken in fp32, before that rounding).  No workspace.
  * A K that is not finite reaches the rows that see it; a V that is not also
  * the rows before it that share its 128-key tile.
- * PA_ERR_UNSUPPORTED as well when (total_tokens / 16 + num_seqs) x n_q_heads
- * reaches 2^31, or num_seqs or n_q_heads exceeds 65535.
+ * PA_ERR_UNSUPPORTED as well when total_tokens x n_q_heads or (total_tokens / 16 +
+ * num_seqs) x n_q_heads reaches 2^31, or num_seqs or n_q_heads exceeds 65535.
  */
 pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
                             const int32_t* query_start_loc, float scale, int n_q_heads,

@@ -76,6 +76,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -186,38 +191,23 @@ __device__ __forceinline__ float tile_weights(const float* x, float sl, float ne
 
 // ------------------------------------------------------------------ output
 // A warp's 32 rows of O leave through the 16x256b shape: four threads hold 8
-// adjacent columns of a row, so that one store of the warp covers 8 rows by 64
-// bytes (16-bit output, after a 4 x 4 exchange within each four threads) or 8
-// rows by 32 bytes (fp32).  A thread storing its own row instead touches 32
-// lines with every store: 2 us a tile for the SM's one store path, measured.
+// adjacent columns of a row, so that one store of the warp covers 8 rows by 32
+// bytes, whole sectors (for 16-bit output after an exchange between
+// neighbours).  A thread storing its own row instead touches 32 lines with
+// every store: 403 against 344 us on 16 ragged prompts.
 
-// thread q of four gives word j and gets word q of thread j, for j = 0 .. 3
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4]) {
-  const bool o1 = threadIdx.x & 1, o2 = threadIdx.x & 2;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const uint32_t r = __shfl_xor_sync(0xffffffffu, o1 ? w[i] : w[i + 1], 1);
-    if (o1) w[i] = r; else w[i + 1] = r;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t r = __shfl_xor_sync(0xffffffffu, o2 ? w[i] : w[i + 2], 2);
-    if (o2) w[i] = r; else w[i + 2] = r;
-  }
-}
-
-// Writes 64 columns of the warp's 32 rows: w0 x the ones at TMEM address ta
-// (plus w1 x the ones at tb when TWO), where a weight of zero makes them zero
-// whatever O holds.  row, w0 and w1 are those of the row that this thread has
-// by number (row = where its 64 values go, null: nowhere); OutT is the output
-// type (16-bit), or float.
-template <typename OutT, bool TWO>
-__device__ __forceinline__ void store_rows(uint32_t ta, uint32_t tb, OutT* row, float w0,
-                                           float w1) {
+// Writes 64 columns of the warp's 32 rows: w0 x the ones at TMEM address ta, plus
+// w1 x the ones at tb when TWO.  row (this thread's row of an array
+// of rows of LD elements at `base`; negative: none), w0 and w1 are those of the
+// row that this thread has by number; OutT is the output type (16-bit), or
+// float.
+template <typename OutT, bool TWO, int LD>
+__device__ __forceinline__ void store_rows(uint32_t ta, uint32_t tb, OutT* base, int row,
+                                           float w0, float w1) {
   constexpr bool kBf = std::is_same<OutT, __nv_bfloat16>::value;
   const int lane = threadIdx.x & 31, q = lane & 3;
-  const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
-  const uint32_t rows = __ballot_sync(0xffffffffu, row != nullptr);
+  const bool odd = q & 1;
+  const uint32_t rows = __ballot_sync(0xffffffffu, row >= 0);
 #pragma unroll 1
   for (int hf = 0; hf < 2; ++hf) {  // rows 0 .. 15, then 16 .. 31
     if ((rows >> (16 * hf) & 0xffffu) == 0) continue;
@@ -228,30 +218,37 @@ __device__ __forceinline__ void store_rows(uint32_t ta, uint32_t tb, OutT* row, 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // rows lane / 4 and lane / 4 + 8 of them
       const int src = 16 * hf + 8 * i + (lane >> 2);
-      OutT* out = reinterpret_cast<OutT*>(__shfl_sync(0xffffffffu, mine, src));
+      const int r = __shfl_sync(0xffffffffu, row, src);
       const float v0 = __shfl_sync(0xffffffffu, w0, src);
-      const float v1 = TWO ? __shfl_sync(0xffffffffu, w1, src) : 0.f;
-      float y[16];  // columns 8 k + 2 q, + 1
+      OutT* out = base + (long long)r * LD;
+      uint64_t y[8];  // columns 8 k + 2 q, + 1
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int e = 4 * (k >> 1) + 2 * i + (k & 1);
-        y[k] = v0 == 0.f ? 0.f : __uint_as_float(a[e]) * v0;
-        if constexpr (TWO) y[k] += v1 == 0.f ? 0.f : __uint_as_float(b[e]) * v1;
+      for (int k = 0; k < 8; ++k)
+        y[k] = mul2(f2(__uint_as_float(a[4 * k + 2 * i]), __uint_as_float(a[4 * k + 2 * i + 1])),
+                    f2(v0, v0));
+      if constexpr (TWO) {
+        const float v1 = __shfl_sync(0xffffffffu, w1, src);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          y[k] = fma2(f2(__uint_as_float(b[4 * k + 2 * i]), __uint_as_float(b[4 * k + 2 * i + 1])),
+                      f2(v1, v1), y[k]);
       }
       if constexpr (std::is_same<OutT, float>::value) {
-        if (out)
+        if (r >= 0)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float2*>(out + 8 * k + 2 * q) = make_float2(y[2 * k], y[2 * k + 1]);
+            *reinterpret_cast<uint64_t*>(out + 8 * k + 2 * q) = y[k];
       } else {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = pack2<kBf>(y[8 * g + 2 * k], y[8 * g + 2 * k + 1]);
-          quad_transpose(w);
-          if (out)
-            *reinterpret_cast<uint4*>(out + 32 * g + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 8; k += 2) {  // even threads take group k, odd ones k + 1
+          float x0, x1, z0, z1;
+          un2(y[k], x0, x1);
+          un2(y[k + 1], z0, z1);
+          const uint32_t x = pack2<kBf>(x0, x1), z = pack2<kBf>(z0, z1);
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x : z, 1);
+          if (r >= 0)
+            *reinterpret_cast<uint2*>(out + 8 * (k + odd) + 4 * (q >> 1)) =
+                odd ? make_uint2(got, z) : make_uint2(x, got);
         }
       }
       __syncwarp();

@@ -786,7 +786,8 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
   if (n_q_heads > 65535 || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   if (!(scale == scale)) return PA_ERR_INVALID_ARG;
   // the kernel counts (sequence, 16 queries or more, head) items in 31 bits
-  if (((int64_t)total_tokens / 16 + num_seqs + 1) * n_q_heads >= (int64_t(1) << 31))
+  if (((int64_t)total_tokens / 16 + num_seqs + 1) * n_q_heads >= (int64_t(1) << 31) ||
+      (int64_t)total_tokens * n_q_heads >= (int64_t(1) << 31))  // rows of out, too
     return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || total_tokens == 0) return PA_OK;
   if (!out || !q || !k || !v || !query_start_loc) return PA_ERR_INVALID_ARG;

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = tc::idesc_f16(BF16, false, kTileM, 0);  // N by tile
     constexpr uint32_t idesc_pv = tc::idesc_f16(BF16, true, kTileM, D);
     constexpr uint64_t kOpStep = L::kOp >> 4;  // descriptors count 16 bytes
+    constexpr bool kTurns = !L::kSepP;
     const int x = warp - kMmaWarp;
     const uint64_t dQ = tc::smem_desc(sbase + L::kQOff + x * L::kOp),
                    dK = tc::smem_desc(sbase + L::kKVOff),
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = max(it.nkt[0], it.nkt[1]), mine = x ? it.nkt[1] : it.nkt[0];
       const int ends = last_parts(it, x, QT);  // of the last key tile
       if (mine > 0) ok = wait_all(&B->q_full[x], items & 1, B, p.dev_err);
-      for (int j = 0; j <= n && ok; ++j, c += 2, ++turns) {
+      for (int j = 0; j <= n && ok; ++j, c += 2) {
         const uint32_t cv = c - 1;
         const int sk = c % NS, sv = cv % NS;
         const bool do_pv = j > 0 && j <= mine, do_s = j < mine;
@@ -228,8 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && wait_all(&B->o_free[x], (items - 1) & 1, B, p.dev_err);
           ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
         }
-        if (!L::kSepP && (x > 0 || turns > 0))
-          ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+        // (an item's first S goes ahead out of turn)
+        if (kTurns && j > 0) {
+          if (x > 0 || turns > 0)
+            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+          ++turns;
+        }
         if (!ok) break;
         if (do_pv) {
           const int nk = j == mine ? 2 * ends : 8;  // 16 keys a step = two 8-row groups of V
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!L::kSepP && do_s) scores(k, j == mine - 1, j == mine - 1 ? ends : 4);
         if (tc::elect_one()) {
-          if (!L::kSepP) mbar_arrive(&B->turn[x ^ 1]);
+          if (kTurns && j > 0) mbar_arrive(&B->turn[x ^ 1]);
           // a stage is free once both warps' MMAs on it are done
           if (j > 0) tc::commit(&B->empty[sv]);
           if (j < n) tc::commit(&B->empty[sk]);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       bool ok = true;
       uint32_t c = 0;
-      int nq[2] = {0, 0};
+      int nq0 = 0, nq1 = 0;  // Q tiles of A and B
       auto tile = [&](const CUtensorMap* map, int kvh, int row, bool tail) {
         const int st = c % NS;
         if (c >= (uint32_t)NS && !wait_ok(&B->empty[st], ((c / NS) - 1) & 1, B, p.dev_err))
@@ -296,33 +301,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++c;
         return true;
       };
+      auto query = [&](int x) {
+        if (!ok || (x ? it.nkt[1] : it.nkt[0]) == 0) return;
+        int& used = x ? nq1 : nq0;
+        if (used > 0) ok = wait_ok(&B->q_empty[x], (used - 1) & 1, B, p.dev_err);
+        if (!ok) return;
+        ++used;
+        uint8_t* d = smem + L::kQOff + x * L::kOp;
+        mbar_arrive_expect_tx(&B->q_full[x], L::kOp);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tc::tma_load_3d(d + h * 16384, &tmq, &B->q_full[x], 64 * h, it.h0,
+                          it.start + it.i0 + x * QT);
+      };
       while (ok && rd.next(B, p.dev_err, it)) {
         rd.done(B);
         const int n = max(it.nkt[0], it.nkt[1]), kvh = it.h0 / p.group;
         for (int j = 0; j < n && ok; ++j) {
-          ok = tile(&tmk, kvh, it.start + j * kTileN, false);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || j > 0 || it.nkt[x] == 0) continue;
-            if (nq[x] > 0) ok = wait_ok(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
-            if (!ok) continue;
-            ++nq[x];
-            uint8_t* d = smem + L::kQOff + x * L::kOp;
-            mbar_arrive_expect_tx(&B->q_full[x], L::kOp);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tc::tma_load_3d(d + h * 16384, &tmq, &B->q_full[x], 64 * h, it.h0,
-                              it.start + it.i0 + x * QT);
-          }
+          // Q of A is free to load long before a stage is, Q of B a little after
+          if (j == 0) query(0);
+          ok = ok && tile(&tmk, kvh, it.start + j * kTileN, false);
+          if (j == 0) query(1);
           ok = ok && tile(&tmv, kvh, it.start + j * kTileN, (j + 1) * kTileN > it.len);
         }
       }
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
         mbar_wait(&B->full[u % NS], (u / NS) & 1);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
+      if (nq0 > 0) mbar_wait(&B->q_full[0], (nq0 - 1) & 1);
+      if (nq1 > 0) mbar_wait(&B->q_full[1], (nq1 - 1) & 1);
     }
   } else if (warp == kSchedWarp) {
     // ------------------------------------------------------------ scheduler
@@ -526,14 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_mine;
       const bool valid = qi < it.len;
       const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
-      T16* out = static_cast<T16*>(p.out) +
-                 ((size_t)(it.start + qi) * p.n_q + it.h0 + (r & ((1 << lhb) - 1))) * D;
-      if (!valid) out = nullptr;
+      const int row = valid ? (it.start + qi) * p.n_q + it.h0 + (r & ((1 << lhb) - 1)) : -1;
       tc::fence_after();
       if (live) {
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 64)
-          attn::store_rows<T16, false>(tO + cc, 0, out ? out + cc : nullptr, inv, 0.f);
+          attn::store_rows<T16, false, D>(tO + cc, 0, static_cast<T16*>(p.out) + cc, row, inv, 0.f);
         tc::fence_before();
       }
       mbar_arrive(&B->o_free[x]);

@@ -860,18 +860,18 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         p.ws_ml[slot] = make_float2(m, l);
       }
       if (live && !(SPLIT && D == 64 && x == 1)) {
+        // (B without a key tile: its O may hold anything, its weight is zero)
         const uint32_t ta = tmem + L::tO(SPLIT ? 0 : x) + lanes + c0,
-                       tb = tmem + L::tO(1) + lanes + c0;
+                       tb = tmem + L::tO(nt > 1 ? 1 : 0) + lanes + c0;
 #pragma unroll 1
         for (int cc = 0; cc < D; cc += 64) {
           if (SPLIT && D == 128 && cc > 0) break;  // 64 of 128 columns each
           if (g.slot < 0)
-            attn::store_rows<T16, SPLIT>(
-                ta + cc, tb + cc,
-                valid ? static_cast<T16*>(p.out) + row * D + c0 + cc : nullptr, w0, w1);
+            attn::store_rows<T16, SPLIT, D>(ta + cc, tb + cc, static_cast<T16*>(p.out) + c0 + cc,
+                                            valid ? (int)row : -1, w0, w1);
           else
-            attn::store_rows<float, SPLIT>(ta + cc, tb + cc,
-                                           valid ? p.ws_o + slot * D + c0 + cc : nullptr, w0, w1);
+            attn::store_rows<float, SPLIT, D>(ta + cc, tb + cc, p.ws_o + c0 + cc,
+                                              valid ? (int)slot : -1, w0, w1);
         }
       }
       tc::fence_before();
