@@ -123,17 +123,19 @@ __device__ __forceinline__ float tile_max(float (&x)[kTileN], bool full, const u
 }
 
 // The same 64 keys at a time, for kernels whose threads cannot hold 128 scores:
-// the maximum is taken on one reading of S, the weights on another.
-__device__ __forceinline__ void load_half(uint32_t ts, int h, bool full, const uint32_t (&vis)[4],
+// the maximum is taken on one reading of S, the weights on another.  The 64
+// scores at `ts`, masked by the two words of vis unless full (then in log2
+// units).
+__device__ __forceinline__ void load_half(uint32_t ts, bool full, uint32_t vis0, uint32_t vis1,
                                           float sl, float (&x)[64]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  tc::ld32x32b_x32(ts + 64 * h, r);
-  tc::ld32x32b_x32(ts + 64 * h + 32, r + 32);
+  tc::ld32x32b_x32(ts, r);
+  tc::ld32x32b_x32(ts + 32, r + 32);
   tc::wait_ld();
   if (!full) {
 #pragma unroll
     for (int e = 0; e < 64; ++e)
-      x[e] = (vis[2 * h + (e >> 5)] >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
+      x[e] = ((e < 32 ? vis0 : vis1) >> (e & 31)) & 1u ? x[e] * sl : -INFINITY;
   }
 }
 __device__ __forceinline__ float tile_max_halves(uint32_t ts, bool full, const uint32_t (&vis)[4],
@@ -142,8 +144,7 @@ __device__ __forceinline__ float tile_max_halves(uint32_t ts, bool full, const u
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     float x[64];
-    const uint32_t v[4] = {h ? vis[2] : vis[0], h ? vis[3] : vis[1], 0u, 0u};
-    load_half(ts + 64 * h, 0, full, v, sl, x);
+    load_half(ts + 64 * h, full, h ? vis[2] : vis[0], h ? vis[3] : vis[1], sl, x);
 #pragma unroll
     for (int e = 0; e < 64; e += 8)
 #pragma unroll

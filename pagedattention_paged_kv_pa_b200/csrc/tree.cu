@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           if (!ok) break;
           const uint8_t* src = smem + L::kRawOff + ((vop ? RS : 0) + rs) * L::kRaw;
           uint8_t* dst = smem + (vop ? L::kVOff : L::kKOff) + st * L::kOp;
-#pragma unroll
+#pragma unroll 2
           for (int m = 0; m < kCh; ++m) {
             // 8 lanes take 8 rows of one chunk, then the next chunk: their
             // 16-byte stores fall into different banks (the swizzle turns with
@@ -782,27 +782,27 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           // a row that has seen no key yet: its weights are 0
           const float neg_m = m == -INFINITY ? 0.f : -m;
           uint32_t pk[32];
-          if constexpr (FP8) attn::load_half(tS, 0, full, vis, sl, s);
-          l += attn::tile_weights<kOpBf16, 64>(s, sle, neg_m, pk);
-          if (L::kSepP && t > 0) {  // P of the tile before has been read
-            ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
-            if (!ok) break;
-            tc::fence_after();
-          }
-          tc::st32x32b_x32(tP, pk);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&B->p_half[x]);
-          if constexpr (FP8) attn::load_half(tS, 1, full, vis, sl, s);
-          if (FP8 && L::kSepP) {
+#pragma unroll(FP8 ? 1 : 2)
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (FP8) {
+              attn::load_half(tS + 64 * h, full, h ? vis[2] : vis[0], h ? vis[3] : vis[1], sl, s);
+              if (L::kSepP && h == 1) {
+                tc::fence_before();
+                mbar_arrive(&B->s_empty[x]);
+              }
+            }
+            l += attn::tile_weights<kOpBf16, 64>(s + (FP8 ? 0 : 64 * h), sle, neg_m, pk);
+            if (L::kSepP && h == 0 && t > 0) {  // P of the tile before has been read
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              if (!ok) break;
+              tc::fence_after();
+            }
+            tc::st32x32b_x32(tP + 32 * h, pk);
+            tc::wait_st();
             tc::fence_before();
-            mbar_arrive(&B->s_empty[x]);
+            mbar_arrive(h ? &B->p_full[x] : &B->p_half[x]);
           }
-          l += attn::tile_weights<kOpBf16, 64>(s + (FP8 ? 0 : 64), sle, neg_m, pk);
-          tc::st32x32b_x32(tP + 32, pk);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&B->p_full[x]);
+          if (!ok) break;
         } else {
           if (L::kSepP) {
             mbar_arrive(&B->s_empty[x]);
