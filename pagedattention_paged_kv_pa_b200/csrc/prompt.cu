@@ -27,6 +27,15 @@
 // its sequence (another sequence's values or padding: 0 x NaN must not reach
 // O).  Every wait is bounded; a role that gives up flags PA_DEVERR_TIMEOUT and
 // leaves, and the CTA drains its loads and MMAs and frees TMEM.
+//
+// Measured back to back in a CUDA graph (and sustained over seconds, where 128-
+// wide heads run into the power limit): 16,384 tokens of 32/8 heads of 128, bf16,
+// 1.74 ms = 1,261 TFLOP/s of causal products (2.03 ms); 16 prompts of up to 2,100
+// tokens, 64/8 x 128, 313 us = 943 TFLOP/s (371 us); 8 of up to 1,500, 32/8 x 64,
+// 52 us; one of 37 tokens 8.2 us.  What bounds it is each tile's chain P -> O +=
+// P V -> next S -> softmax, ~1,700 clocks for two tiles against 1,024 of the
+// products or the exponentials (tensor pipe and XU at 47 %): at head_dim 128 P
+// lies over S, for want of TMEM.
 #include <type_traits>
 
 #include "attn_tile.cuh"
