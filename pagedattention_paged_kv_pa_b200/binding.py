@@ -8,6 +8,7 @@ library is missing this module raises on import -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -244,6 +245,16 @@ def pa_decode_multi(out, q, k_pool, v_pool, block_tables, context_lens, scale, k
     return out
 
 
+def _allocating_on(dev: int, stream):
+    """Memory of tensors made inside is `stream`'s to use again: freed on return
+    while the launch still uses it, it goes to later work of that stream only."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
 def pa_decode_tree_workspace_size(num_seqs: int, q_len: int, n_q_heads: int, n_kv_heads: int,
                                   head_dim: int) -> int:
     return lib.pa_decode_tree_workspace_size(num_seqs, q_len, n_q_heads, n_kv_heads, head_dim)
@@ -299,7 +310,8 @@ def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, sc
     if masks.dtype != torch.int64 or out.dtype != q.dtype or v_pool.dtype != k_pool.dtype:
         raise PAError(PA_ERR_INVALID_ARG, "pa_decode_tree dtypes")
     if workspace is None:
-        workspace = alloc_tree_workspace(q, k_pool)
+        with _allocating_on(dev, stream):
+            workspace = alloc_tree_workspace(q, k_pool)
     _launch(dev, stream, "pa_decode_tree", lib.pa_decode_tree, out.data_ptr(), q.data_ptr(),
             k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
             context_lens.data_ptr(), masks.data_ptr(), _ptr(tree_lens), scale, bs, n_q, n_kv, d,

@@ -326,3 +326,28 @@ def test_captured_graphs_with_a_workspace_each(B, cuda_device):
     torch.cuda.synchronize()
     for i, (c, o) in enumerate(zip(cs, outs)):
         c.check(o, f"graph {i}")
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_own_workspace_belongs_to_the_calls_stream(B, cuda_device, as_int, monkeypatch):
+    c = Case([1500, 3, 900], 16, 8, 2, 128, torch.bfloat16, False, cuda_device, seed=23)
+    a, k = c.args()
+    out = torch.full_like(c.q, 7.0)
+    made = []
+    alloc = B.alloc_tree_workspace
+
+    def recorded(*x):
+        w = alloc(*x)
+        made.append((w.data_ptr(), w.numel()))
+        return w
+
+    monkeypatch.setattr(B, "alloc_tree_workspace", recorded)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    B.pa_decode_tree(out, *a, **k, stream=side.cuda_stream if as_int else side)
+    # what the current stream allocates next is not the memory in use there
+    other = torch.empty(made[0][1], dtype=torch.uint8, device=cuda_device)
+    assert other.data_ptr() != made[0][0]
+    other.fill_(0x7f)
+    torch.cuda.synchronize()
+    c.check(out, "own workspace")
