@@ -212,7 +212,7 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_pool, const vo
  * nobody.  What lies in the cache past the context is never used.
  *
  *   out, q       device [num_seqs][q_len][n_q_heads][head_dim], dtype q_dtype;
- *                must not overlap
+ *                must not overlap (PA_ERR_INVALID_ARG)
  *   q_len        1 .. 64, the most nodes of a sequence
  *   masks        device uint64 [num_seqs][q_len], 8-byte aligned
  *   tree_lens    device int32 [num_seqs], each in [0, q_len]; NULL: all q_len.
@@ -454,7 +454,7 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  * there is not used; sequences may be empty.
  *
  *   out            device [total_tokens][n_q_heads][head_dim], packed; must not
- *                  overlap q, k or v
+ *                  overlap q, k or v (PA_ERR_INVALID_ARG)
  *   q, k, v        device, token t at element t * stride: [n_q_heads] resp.
  *                  [n_kv_heads][head_dim] elements, so the parts of one fused
  *                  projection need no copy; strides in elements, multiples of
@@ -556,7 +556,8 @@ pa_status pa_swap_blocks(void* dst_k_pool, void* dst_v_pool, const void* src_k_p
  * before any is written.  The sequence then holds P_s + accepted_lens[s]
  * tokens (pa_alloc_truncate); rows behind them are left as they are.
  *
- *   k_pools, v_pools  host arrays of n_layers device pools (see conventions)
+ *   k_pools, v_pools  host arrays of n_layers device pools (see conventions), no
+ *                  two of which may overlap (PA_ERR_INVALID_ARG)
  *   tree_lens      device int32 [num_seqs], or NULL: all q_len
  *   accepted       device int32 [num_seqs][max_accepted], strictly increasing
  *                  node indices below n_s (a path of a tree whose parents come

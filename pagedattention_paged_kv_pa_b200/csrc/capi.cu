@@ -163,6 +163,34 @@ bool q_rows_map(const void* q, int rows, int n_q, int group, int q_len, CUtensor
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether `n` 16-bit elements at `out` share memory with one of `rows` rows of
+// `len` elements, `stride` apart (len <= stride), at x.
+bool rows_overlap(const void* out, int64_t n, const void* x, int64_t rows, int64_t len,
+                  int64_t stride) {
+  const int64_t o = static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) / 2) -
+                    static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) / 2);
+  // the first row that ends behind the start of out
+  const int64_t t = o < len ? 0 : (o - len) / stride + 1;
+  return t < rows && t * stride < o + n;
+}
+
+// PA_ERR_INVALID_ARG if any two of the 2 n_layers pools of `bytes` bytes share
+// memory: their moves would be made twice.
+pa_status check_pools_apart(void* const* k, void* const* v, int n_layers, uint64_t bytes) {
+  std::vector<uintptr_t> at;
+  try {
+    at.reserve(2 * (size_t)n_layers);
+  } catch (...) {
+    return PA_ERR_OOM;
+  }
+  for (int l = 0; l < n_layers; l++) at.push_back(reinterpret_cast<uintptr_t>(k[l]));
+  for (int l = 0; l < n_layers; l++) at.push_back(reinterpret_cast<uintptr_t>(v[l]));
+  std::sort(at.begin(), at.end());
+  for (size_t i = 1; i < at.size(); i++)
+    if (at[i] - at[i - 1] < bytes) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
 // Map over 16-bit rows [tokens][heads][d] with `stride` elements between tokens:
 // one box is 64 columns of `box_h` heads of `box_t` tokens, written as rows
 // token x box_h + head with the 128-byte swizzle; rows past the last token read
@@ -522,6 +550,8 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) ||
       (reinterpret_cast<uintptr_t>(masks) & 7u))
     return PA_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)num_seqs * q_len, qn = (int64_t)n_q_heads * head_dim;
+  if (rows_overlap(out, rows * qn, q, rows, qn, qn)) return PA_ERR_INVALID_ARG;
   const bool fp8 = kv_dtype == PA_FP8_E4M3;
   if (!(scale == scale) || (fp8 && !(k_scale > 0.f && v_scale > 0.f))) return PA_ERR_INVALID_ARG;
   const size_t need =
@@ -799,6 +829,10 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
     return PA_ERR_INVALID_ARG;
   // the tensor maps' strides are 40 bits of bytes
   if (std::max({q_stride, k_stride, v_stride}) >= (int64_t(1) << 38)) return PA_ERR_UNSUPPORTED;
+  if (rows_overlap(out, total_tokens * qn, q, total_tokens, qn, q_stride) ||
+      rows_overlap(out, total_tokens * qn, k, total_tokens, kn, k_stride) ||
+      rows_overlap(out, total_tokens * qn, v, total_tokens, kn, v_stride))
+    return PA_ERR_INVALID_ARG;
   pa::PromptParams p;
   p.out = out;
   p.query_start_loc = query_start_loc;
@@ -952,6 +986,9 @@ pa_status pa_compact_tokens(void* const* k_pools, void* const* v_pools, int n_la
   for (int l = 0; l < n_layers; l++)
     if (!k_pools[l] || !v_pools[l] || !aligned16(k_pools[l]) || !aligned16(v_pools[l]))
       return PA_ERR_INVALID_ARG;
+  const uint64_t pool_bytes = (uint64_t)num_blocks * n_kv_heads * 16 * row;
+  const pa_status apart = check_pools_apart(k_pools, v_pools, n_layers, pool_bytes);
+  if (apart != PA_OK) return apart;
   pa::CompactParams p;
   p.block_tables = block_tables;
   p.context_lens = context_lens;

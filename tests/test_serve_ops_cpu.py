@@ -231,3 +231,27 @@ def test_accepted_ids_bring_prefix_caching_back(B):
     assert st == B.PA_OK
     st, _, n = a.admit(4, full + [52, 53] + list(range(60, 74)) + [1])
     assert st == B.PA_OK and n == 48
+
+
+def test_overlapping_memory_is_refused(B):
+    # out [50][8 x 128] of 102,400 bytes against q, k, v far away
+    far = dict(out=1 << 30, q=1 << 31, k=1 << 32, v=1 << 33)
+    for x, n in (("q", 50 * 1024 * 2), ("k", 50 * 256 * 2), ("v", 50 * 256 * 2)):
+        for at in (1 << 30, (1 << 30) + 102400 - 16, (1 << 30) - n + 16):
+            assert _packed(B, **{**far, x: at}) == B.PA_ERR_INVALID_ARG
+    # a row of a strided k inside out; its first row ends before out
+    assert _packed(B, **{**far, "k": (1 << 30) - 512, "ks": 256 + 8}) == B.PA_ERR_INVALID_ARG
+    at = 1 << 30
+    for q in (at, at + 4 * 10 * 1024 * 2 - 16, at - 4 * 10 * 1024 * 2 + 16):
+        assert _tree(B, out=at, q=q) == B.PA_ERR_INVALID_ARG
+    pool = 100 * 2 * 16 * 128 * 2
+    apart = [pool * i + 16 for i in range(1, 5)]
+    for i in range(4):
+        for j in range(4):
+            if i != j:
+                x = list(apart)
+                x[i] = x[j]
+                assert _compact(B, k=x[:2], v=x[2:]) == B.PA_ERR_INVALID_ARG
+    assert _compact(B, k=apart[:2], v=[apart[2], apart[2] + pool - 16]) == B.PA_ERR_INVALID_ARG
+    many = [pool * i + 16 for i in range(1, 201)]
+    assert _compact(B, k=many[:100], v=many[100:199] + many[:1]) == B.PA_ERR_INVALID_ARG
