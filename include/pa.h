@@ -460,8 +460,9 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
  *                  projection need no copy; strides in elements, multiples of
  *                  8, not below the token's own size
  *   query_start_loc device int32 [num_seqs + 1], non-decreasing, within
- *                  [0, total_tokens].  An entry that is not is flagged with
- *                  PA_DEVERR_QUERY_LOC, its sequence clamped to the tensors
+ *                  [0, total_tokens].  Entries that are not are flagged with
+ *                  PA_DEVERR_QUERY_LOC, and each then counts as the largest of
+ *                  0 and the entries up to it, at most total_tokens
  *   total_tokens   rows of out, q, k and v
  *
  * Supported: dtype F16 or BF16 (of q, k, v and out); head_dim 64 or 128; any

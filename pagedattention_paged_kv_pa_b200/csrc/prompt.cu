@@ -109,12 +109,33 @@ struct Reader {
   __device__ __forceinline__ void done(Bars* B) { mbar_arrive(&B->item_empty[(k - 1) % kItems]); }
 };
 
-// Sequence s: its first row and length (0: nothing to do, or inconsistent).
-__device__ __forceinline__ int seq_span(const PromptParams& p, int s, int& start, bool& bad) {
-  const int a = __ldg(&p.query_start_loc[s]), b = __ldg(&p.query_start_loc[s + 1]);
-  bad = a < 0 || b < a || b > p.total;
-  start = a;
-  return a < 0 || b < a ? 0 : max(0, min(b, p.total) - a);
+// The length of sequence s (0 behind the last one) and its first row, where the
+// starts are in order and within the tensors.
+__device__ __forceinline__ int span_of(const PromptParams& p, int s, int& start) {
+  if (s >= p.num_seqs) return 0;
+  start = __ldg(&p.query_start_loc[s]);
+  return __ldg(&p.query_start_loc[s + 1]) - start;
+}
+// The same of other starts, for the 32 sequences of a warp (s = that of this
+// lane): each start counts as the largest of 0 and the ones up to it, at most
+// `total`, so that no row belongs to two sequences and the items are no more than
+// starts in order have.  `before`: the largest up to these sequences, 0 at first.
+__device__ __forceinline__ int span_in_order(const PromptParams& p, int s, int lane, int& before,
+                                             int& start) {
+  int a = 0, b = 0;
+  if (s < p.num_seqs) {
+    a = min(max(__ldg(&p.query_start_loc[s]), 0), p.total);
+    b = min(max(__ldg(&p.query_start_loc[s + 1]), 0), p.total);
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, a, m);
+    if (lane >= m) a = max(a, v);
+  }
+  start = max(a, before);
+  b = max(b, start);  // the next sequence's start
+  before = __shfl_sync(0xffffffffu, b, 31);
+  return b - start;
 }
 
 // Of the last key tile of item tile X: how many of its four 32-key parts some
@@ -347,21 +368,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and the head groups of each
     const unsigned hgroups = p.n_q >> lhb;
     const int lspan = 8 - lhb, span = 1 << lspan;  // queries of an item
-    auto items_of = [&](int s) -> int {
-      int start;
-      bool bad;
-      return s < p.num_seqs ? (seq_span(p, s, start, bad) + span - 1) >> lspan : 0;
-    };
+    auto items_of = [&](int len) { return (len + span - 1) >> lspan; };
     int top = 0;
+    bool ordered = true;
 #pragma unroll 1
     for (int s = lane; s < p.num_seqs; s += 32) {
-      int start;
-      bool bad;
-      top = max(top, (seq_span(p, s, start, bad) + span - 1) >> lspan);
-      if (bad && blockIdx.x == 0) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
+      const int a = __ldg(&p.query_start_loc[s]), b = __ldg(&p.query_start_loc[s + 1]);
+      if (a < 0 || b < a || b > p.total)
+        ordered = false;
+      else
+        top = max(top, items_of(b - a));
+    }
+    ordered = __all_sync(0xffffffffu, ordered);
+    if (!ordered) {
+      if (blockIdx.x == 0 && lane == 0) flag_error(p.dev_err, PA_DEVERR_QUERY_LOC);
+      top = 0;
+      int start, before = 0;
+#pragma unroll 1
+      for (int s0 = 0; s0 < p.num_seqs; s0 += 32)
+        top = max(top, items_of(span_in_order(p, s0 + lane, lane, before, start)));
     }
     for (int m = 16; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const int first = items_of(lane);  // of the first 32 sequences, kept
+    // the first 32 sequences, kept
+    int start0 = 0, before0 = 0;
+    const int len0 = ordered ? span_of(p, lane, start0)
+                             : span_in_order(p, lane, lane, before0, start0);
     int level = top, cnt = 0;
     unsigned base = 0;  // (sequence, level) pairs before this level
     bool more = true;
@@ -378,27 +409,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (level < 0) {
           more = false;
         } else {
-          int n = first > level;
+          int n = items_of(len0) > level, start, before = before0;
 #pragma unroll 1
-          for (int s = 32 + lane; s < p.num_seqs; s += 32) n += items_of(s) > level;
+          for (int s0 = 32; s0 < p.num_seqs; s0 += 32)
+            n += items_of(ordered ? span_of(p, s0 + lane, start)
+                                  : span_in_order(p, s0 + lane, lane, before, start)) > level;
           cnt = __reduce_add_sync(0xffffffffu, n);
         }
       }
       Item it;
       it.start = -1;
+      it.len = 0;
       if (more) {
-        int r = (int)(want - base), seq = -1;
+        int r = (int)(want - base), start = start0, len = len0, before = before0;
 #pragma unroll 1
-        for (int s0 = 0; seq < 0 && s0 < p.num_seqs; s0 += 32) {
-          const bool has = (s0 == 0 ? first : items_of(s0 + lane)) > level;
+        for (int s0 = 0;;) {
+          const bool has = items_of(len) > level;
           const uint32_t m = __ballot_sync(0xffffffffu, has);
           const uint32_t hit = __ballot_sync(
               0xffffffffu, has && __popc(m & ((1u << lane) - 1u)) == r);
-          if (hit) seq = s0 + __ffs(hit) - 1;
+          if (hit) {
+            it.start = __shfl_sync(0xffffffffu, start, __ffs(hit) - 1);
+            it.len = __shfl_sync(0xffffffffu, len, __ffs(hit) - 1);
+            break;
+          }
           r -= __popc(m);
+          s0 += 32;
+          if (s0 >= p.num_seqs) break;  // (the level's items were counted: not reached)
+          len = ordered ? span_of(p, s0 + lane, start)
+                        : span_in_order(p, s0 + lane, lane, before, start);
         }
-        bool bad;
-        it.len = seq_span(p, max(seq, 0), it.start, bad);
+        more = it.start >= 0;
         // of an odd number of tiles the first, which sees the fewest keys, is
         // alone in its item
         const bool odd = ((it.len + QT - 1) >> (lspan - 1)) & 1;

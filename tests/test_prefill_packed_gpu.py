@@ -155,6 +155,25 @@ def test_inconsistent_starts_are_flagged_and_stay_in_bounds(B, cuda_device):
     assert (out[40:] == 7).all()
 
 
+@pytest.mark.parametrize("starts", [
+    [-5, 40], [0, 40, 30, 150], [-300, -200, 7], [500, 3], [0, 100] * 40 + [0, 100],
+    [20, 10, 60, 50, 200, -1, 80], [0, 10, 5] + [11 + i for i in range(90)],
+    [3] * 30 + [2, 50, 49, 48, 47, 77, 500], [i + (37 * i) % 29 - 12 for i in range(96)], [2 ** 31 - 1, -2 ** 31, 60, 40]],
+    ids=lambda x: f"{len(x) - 1}_{x[0]}_{x[1]}")
+def test_starts_out_of_order_count_as_the_largest_so_far(B, cuda_device, starts):
+    # every row has one owner and the sequences are those of the running maximum
+    total = 100
+    q, k, v, _ = make([total], 16, 1, 64, torch.bfloat16, cuda_device, seed=15)
+    at = torch.tensor(starts).clamp(0, total).cummax(0).values
+    assert at.tolist() != starts
+    out, err = run(B, q, k, v, torch.tensor(starts, dtype=torch.int32, device=cuda_device), 0.125)
+    assert err == B.PA_DEVERR_QUERY_LOC
+    assert (out[:at[0]] == 7).all() and (out[at[-1]:] == 7).all()
+    check(out, q, k, v, at.diff().tolist(), 0.125, f"{starts[:8]}", at=int(at[0]))
+    same, err = run(B, q, k, v, at.to(torch.int32).to(cuda_device), 0.125)
+    assert err == 0 and torch.equal(out, same)
+
+
 def test_captured_and_replayed_with_other_lengths(B, cuda_device):
     lens = [50, 300, 17]
     q, k, v, start = make(lens, 8, 2, 128, torch.bfloat16, cuda_device, seed=11)
