@@ -114,7 +114,7 @@ struct Reader {
 __device__ __forceinline__ int span_of(const PromptParams& p, int s, int& start) {
   if (s >= p.num_seqs) return 0;
   start = __ldg(&p.query_start_loc[s]);
-  return __ldg(&p.query_start_loc[s + 1]) - start;
+  return (int)((uint32_t)__ldg(&p.query_start_loc[s + 1]) - (uint32_t)start);
 }
 // The same of other starts, for the 32 sequences of a warp (s = that of this
 // lane): each start counts as the largest of 0 and the ones up to it, at most
@@ -369,15 +369,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned hgroups = p.n_q >> lhb;
     const int lspan = 8 - lhb, span = 1 << lspan;  // queries of an item
     auto items_of = [&](int len) { return (len + span - 1) >> lspan; };
+    // the first 32 sequences, kept
+    int start0 = 0, len0 = span_of(p, lane, start0), before0 = 0;
     int top = 0;
     bool ordered = true;
 #pragma unroll 1
-    for (int s = lane; s < p.num_seqs; s += 32) {
-      const int a = __ldg(&p.query_start_loc[s]), b = __ldg(&p.query_start_loc[s + 1]);
-      if (a < 0 || b < a || b > p.total)
+    for (int s = lane, a = start0, n = len0; s < p.num_seqs;) {
+      // (a negative end gives n < 0 or, wrapped, a + n >= 2^31)
+      if (a < 0 || n < 0 || n > p.total - a)
         ordered = false;
       else
-        top = max(top, items_of(b - a));
+        top = max(top, items_of(n));
+      s += 32;
+      n = span_of(p, s, a);
     }
     ordered = __all_sync(0xffffffffu, ordered);
     if (!ordered) {
@@ -389,10 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = max(top, items_of(span_in_order(p, s0 + lane, lane, before, start)));
     }
     for (int m = 16; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    // the first 32 sequences, kept
-    int start0 = 0, before0 = 0;
-    const int len0 = ordered ? span_of(p, lane, start0)
-                             : span_in_order(p, lane, lane, before0, start0);
+    if (!ordered) len0 = span_in_order(p, lane, lane, before0, start0);
     int level = top, cnt = 0;
     unsigned base = 0;  // (sequence, level) pairs before this level
     bool more = true;
