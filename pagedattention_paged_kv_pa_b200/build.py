@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libpa_b200.so")
 OBJDIR = os.path.join(ROOT, "_build", "obj")
 
 SOURCES = ["capi.cu", "decode.cu", "decode_multi_tc.cu", "cache_ops.cu", "prefill.cu",
-           "allocator.cpp", "decode_noalloc.cu", "prompt.cu", "tree.cu", "compact.cu"]
+           "allocator.cpp", "decode_noalloc.cu", "prompt.cu", "tree.cu", "compact.cu",
+           "device_info.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
