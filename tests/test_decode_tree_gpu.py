@@ -1,5 +1,7 @@
 """pa_decode_tree (a tree of drafted tokens over the paged cache) against the
 64-bit form."""
+import math
+
 import pytest
 import torch
 
@@ -212,6 +214,70 @@ def test_scales(B, cuda_device, scale):
     c = Case([200, 33, 700], 6, 8, 2, 128, torch.bfloat16, False, cuda_device, seed=14)
     c.scale = scale
     c.check(c.run(B), f"scale {scale}")
+
+
+def staircase(c, unit):
+    """Keys and queries for which a row's maximum grows by 9 (in log2 units, more
+    than the kernel's lazy limit of 8) again and again: `unit` tiles of 128 keys
+    on one level, then `unit` tiles where one key lies 9 above it and the others at
+    0.  The 128 weights of 2^-9 that such a jump leaves behind are a fifth of the
+    sum, and V is positive on the levels and negative between them, so a wrong
+    factor shows.  Levels are whole numbers N / 8, N the sum of a
+    key's small whole components, exact in every type and in the fp32 sums (N <
+    1,024; N / 8 log2 e within 2^-17, far below what plain64 counts for scores).
+    Odd heads get -q, for which the keys fall."""
+    d = c.q.shape[-1]
+    for s, n in enumerate(c.ctx):
+        p = torch.arange(n)
+        u = p // (128 * unit)
+        spike = (u % 2 == 1) & (p % (128 * unit) == 37 + s)
+        N = torch.where(u % 2 == 0, 72 * (u // 2), torch.where(spike, 72 * (u // 2 + 1), 0))
+        assert n == 0 or N.max() < 1024
+        rows = (N[:, None] // d + (torch.arange(d) < N[:, None] % d)).to(c.dev)
+        rows = rows.to(torch.float8_e4m3fn).view(torch.uint8) if c.fp8 else rows.to(c.k.dtype)
+        at = c.tables[s, p // 16].long().to(c.dev), slice(None), (p % 16).to(c.dev)
+        c.k[at] = rows[:, None]
+        neg = (u % 2 == 1)[:, None, None].to(c.dev)
+        v = c.v[at]
+        c.v[at] = torch.where(neg, v | 0x80, v & 0x7f) if c.fp8 else \
+            torch.where(neg, -v.abs(), v.abs())
+    c.q[:] = 1.0
+    c.q[:, :, 1::2] = -1.0
+    c.k_scale = 0.5 if c.fp8 else 1.0
+    c.scale = math.log(2.0) / 8 / c.k_scale
+
+
+@pytest.mark.parametrize("dt,fp8", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes,G,unit", [(7, 4, 1), (7, 4, 2), (16, 8, 2), (40, 4, 1), (33, 8, 1),
+                                          (64, 8, 2)])
+def test_growing_scores_rescale(B, cuda_device, dt, fp8, d, nodes, G, unit):
+    # 24 sequences of 3 kv heads: units cut into segments of several tiles, whose
+    # maxima differ by tens, contexts that end on different steps of the stairs
+    # (most just behind a jump)
+    ctx = [unit * 128 * (2 * k + 1) + r for k in (0, 1, 4, 7, 10, 12) for r in (70, 91, 127, -30)]
+    c = Case(ctx, nodes, 3 * G, 3, d, dt, fp8, cuda_device, seed=50,
+             lens=[max(1, nodes - 5 * (i % 3)) for i in range(24)])
+    staircase(c, unit)
+    c.check(c.run(B), f"staircase of {unit}, {dt} fp8={fp8} d={d} nodes={nodes} G={G}")
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes,G", [(6, 4), (16, 8), (40, 4), (64, 8)])
+def test_rows_of_very_different_sizes_over_fp8(B, cuda_device, dt, d, nodes, G):
+    # over an E4M3 cache a bf16 row is brought into f16's range by a power of two of its
+    # own: neighbouring nodes, heads and sequences differ here, and a CTA works on
+    # several sequences one after another
+    ctx = [(97 * i) % 400 for i in range(300)]
+    c = Case(ctx, nodes, 2 * G, 2, d, dt, True, cuda_device, seed=51,
+             lens=[(i * 7) % (nodes + 1) for i in range(300)])
+    at = [torch.arange(n, device=cuda_device) for n in c.q.shape[:3]]
+    e = (7 * at[0][:, None, None] + 5 * at[1][:, None] + 3 * at[2]) % 13
+    if dt == torch.bfloat16:
+        e = torch.where(e == 11, 40, torch.where(e == 12, 100, e))
+    c.q = (c.q.double() * torch.exp2(-e.double())[..., None]).to(dt)
+    c.check(c.run(B), f"{dt} d={d} nodes={nodes} G={G}")
 
 
 def test_captured_and_replayed_with_other_contexts(B, cuda_device):
