@@ -1,4 +1,6 @@
 """pa_prefill_packed (attention over whole prompts) against the 64-bit form."""
+import math
+
 import pytest
 import torch
 
@@ -141,6 +143,36 @@ def test_growing_scores_rescale(B, cuda_device):
     k[:] = -k
     out, err = run(B, q, k, v, start, 0.5)
     check(out, q, k, v, [n], 0.5, "falling")
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q,n_kv", [(2, 1), (3, 3)])
+def test_small_steps_rescale(B, cuda_device, dt, d, n_q, n_kv):
+    # tiles of 128 keys on one level, then one where a single key lies 9 higher (in
+    # log2 units, the lazy limit is 8) and the others at 0: the 128 weights of 2^-9
+    # it leaves behind are a fifth of a row's sum, with V of the other sign.  Levels
+    # are whole numbers N / 8, N < 1,024 the sum of a key's small whole
+    # components, exact in the fp32 sums; odd heads get -q, for which they fall
+    lens = [3400, 129, 700, 1500]
+    q, k, v, start = make(lens, n_q, n_kv, d, dt, cuda_device, seed=16)
+    q[:] = 1.0
+    q[:, 1::2] = -1.0
+    at = 0
+    for n in lens:
+        p = torch.arange(n, device=cuda_device)
+        u = p // 128
+        top = torch.where(p % 128 == 37, 72 * (u // 2 + 1), 0)
+        N = torch.where(u % 2 == 0, 72 * (u // 2), top)
+        assert N.max() < 1024
+        k[at:at + n] = (N[:, None] // d + (torch.arange(d, device=cuda_device)
+                                           < N[:, None] % d)).to(dt)[:, None]
+        v[at:at + n] = v[at:at + n].abs() * torch.where(u % 2 == 0, 1, -1).to(dt)[:, None, None]
+        at += n
+    scale = math.log(2.0) / 8
+    out, err = run(B, q, k, v, start, scale)
+    assert err == 0
+    check(out, q, k, v, lens, scale, f"steps of 9, {dt} d={d} {n_q}/{n_kv}")
 
 
 def test_inconsistent_starts_are_flagged_and_stay_in_bounds(B, cuda_device):
