@@ -248,6 +248,23 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
                          void* stream);
 
 /*
+ * pa_test_decode_tree_timeout -- pa_test_decode_timeout for pa_decode_tree: the
+ * waits of its attention kernel give up after wait_limit_us microseconds (1 ..
+ * 1,000,000), and every CTA leaves its K tile number skip_tile (128 keys each)
+ * unloaded.
+ */
+pa_status pa_test_decode_tree_timeout(void* out, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables,
+                                      const int32_t* context_lens, const uint64_t* masks,
+                                      const int32_t* tree_lens, float scale, int block_size,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int num_seqs,
+                                      int q_len, int max_blocks_per_seq, int num_blocks,
+                                      pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale,
+                                      float v_scale, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_err, void* stream, int skip_tile,
+                                      uint32_t wait_limit_us);
+
+/*
  * pa_tree_masks -- host helper for pa_decode_tree: the masks of trees given by
  * their parents.  parents[s][i] is the parent of node i, a lower index, or -1
  * for a node that continues the prefix; masks_out[s][i] gets the bits of node
@@ -479,6 +496,19 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
                             int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
                             pa_dtype dtype, int32_t* dev_err, void* stream);
+
+/*
+ * pa_test_prefill_packed_timeout -- pa_test_decode_timeout for
+ * pa_prefill_packed: the waits give up after wait_limit_us microseconds (1 ..
+ * 1,000,000), and every CTA leaves number skip_tile of its K and V tiles (K 0, V
+ * 0, K 1, ...; 128 keys each) unloaded.
+ */
+pa_status pa_test_prefill_packed_timeout(void* out, const void* q, const void* k, const void* v,
+                                         const int32_t* query_start_loc, float scale,
+                                         int n_q_heads, int n_kv_heads, int head_dim, int num_seqs,
+                                         int total_tokens, int64_t q_stride, int64_t k_stride,
+                                         int64_t v_stride, pa_dtype dtype, int32_t* dev_err,
+                                         void* stream, int skip_tile, uint32_t wait_limit_us);
 
 /* ------------------------------------------------------------------------- */
 /* Slot write and copy-on-write block copy                                    */

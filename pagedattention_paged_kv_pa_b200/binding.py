@@ -35,7 +35,7 @@ EXPORTS = (
     "pa_swap_blocks", "pa_decode_shared_prefix", "pa_prefix_groups",
     "pa_prefill_workspace_size", "pa_test_decode_timeout", "pa_decode_tree",
     "pa_decode_tree_workspace_size", "pa_tree_masks", "pa_prefill_packed", "pa_compact_tokens",
-    "pa_alloc_truncate",
+    "pa_alloc_truncate", "pa_test_decode_tree_timeout", "pa_test_prefill_packed_timeout",
 )
 
 
@@ -97,10 +97,13 @@ def _load() -> ctypes.CDLL:
                                           P, P, P, I, I, P, Z, P, P]
     L.pa_decode_tree_workspace_size.argtypes = [I, I, I, I, I]
     L.pa_decode_tree_workspace_size.restype = Z
-    L.pa_decode_tree.argtypes = [P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, F, F,
-                                 P, Z, P, P]
+    tree = [P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, F, F, P, Z, P, P]
+    L.pa_decode_tree.argtypes = tree
+    L.pa_test_decode_tree_timeout.argtypes = tree + [I, ctypes.c_uint32]
     L.pa_tree_masks.argtypes = [P, P, I, I, P]
-    L.pa_prefill_packed.argtypes = [P, P, P, P, P, F, I, I, I, I, I, I64, I64, I64, I, P, P]
+    packed = [P, P, P, P, P, F, I, I, I, I, I, I64, I64, I64, I, P, P]
+    L.pa_prefill_packed.argtypes = packed
+    L.pa_test_prefill_packed_timeout.argtypes = packed + [I, ctypes.c_uint32]
     L.pa_compact_tokens.argtypes = [P, P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
     L.pa_alloc_truncate.argtypes = [P, I64, I, P, I]
     L.pa_prefix_groups.argtypes = [P, P, I, I, I, I, I, P, P, P, P, P]
@@ -110,7 +113,8 @@ def _load() -> ctypes.CDLL:
     L.pa_alloc_cached_list.argtypes = [P, P, I, P]
     L.pa_alloc_num_cached.argtypes = [P]
     for fn in ("pa_decode_tree", "pa_tree_masks", "pa_prefill_packed", "pa_compact_tokens",
-               "pa_alloc_truncate"):
+               "pa_alloc_truncate", "pa_test_decode_tree_timeout",
+               "pa_test_prefill_packed_timeout"):
         getattr(L, fn).restype = I
     for fn in ("pa_alloc_num_tokens", "pa_alloc_refcount", "pa_alloc_num_free",
                "pa_alloc_num_seqs", "pa_alloc_num_cached"):
@@ -287,12 +291,8 @@ def tree_masks(parents: torch.Tensor, tree_lens=None) -> torch.Tensor:
     return out
 
 
-def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, scale,
-                   tree_lens=None, k_scale=1.0, v_scale=1.0, workspace=None, dev_err=None,
-                   stream=None):
-    """Tree decode: q / out are [num_seqs, q_len, n_q, d]; node i of sequence s
-    attends to the context before the tree and to the nodes j whose bit is set
-    in masks[s, i] (int64, see tree_masks)."""
+def _decode_tree(fn, out, q, k_pool, v_pool, block_tables, context_lens, masks, scale, tree_lens,
+                 k_scale, v_scale, workspace, dev_err, stream):
     _contig(out, q, k_pool, v_pool, block_tables, context_lens, masks, tree_lens, workspace)
     dev = _on_device(q, out, k_pool, v_pool, block_tables, context_lens, masks, tree_lens,
                      workspace, dev_err)
@@ -312,12 +312,33 @@ def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, sc
     if workspace is None:
         with _allocating_on(dev, stream):
             workspace = alloc_tree_workspace(q, k_pool)
-    _launch(dev, stream, "pa_decode_tree", lib.pa_decode_tree, out.data_ptr(), q.data_ptr(),
+    _launch(dev, stream, "pa_decode_tree", fn, out.data_ptr(), q.data_ptr(),
             k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
             context_lens.data_ptr(), masks.data_ptr(), _ptr(tree_lens), scale, bs, n_q, n_kv, d,
             num_seqs, q_len, block_tables.shape[1], num_blocks, dtype_code(q), dtype_code(k_pool),
             k_scale, v_scale, workspace.data_ptr(), workspace.nbytes, _ptr(dev_err))
     return out
+
+
+def pa_decode_tree(out, q, k_pool, v_pool, block_tables, context_lens, masks, scale,
+                   tree_lens=None, k_scale=1.0, v_scale=1.0, workspace=None, dev_err=None,
+                   stream=None):
+    """Tree decode: q / out are [num_seqs, q_len, n_q, d]; node i of sequence s
+    attends to the context before the tree and to the nodes j whose bit is set
+    in masks[s, i] (int64, see tree_masks)."""
+    return _decode_tree(lib.pa_decode_tree, out, q, k_pool, v_pool, block_tables, context_lens,
+                        masks, scale, tree_lens, k_scale, v_scale, workspace, dev_err, stream)
+
+
+def pa_test_decode_tree_timeout(out, q, k_pool, v_pool, block_tables, context_lens, masks, scale,
+                                skip_tile: int, wait_limit_us: int, tree_lens=None, k_scale=1.0,
+                                v_scale=1.0, workspace=None, dev_err=None, stream=None):
+    """Test hook: pa_decode_tree with short bounded waits and one K tile left
+    unloaded in every CTA, so the waits run out (see include/pa.h)."""
+    def fn(*a):
+        return lib.pa_test_decode_tree_timeout(*a, int(skip_tile), int(wait_limit_us))
+    return _decode_tree(fn, out, q, k_pool, v_pool, block_tables, context_lens, masks, scale,
+                        tree_lens, k_scale, v_scale, workspace, dev_err, stream)
 
 
 def prefix_groups(block_tables, context_lens, n_q_heads: int, n_kv_heads: int, kv_dtype: int):
@@ -459,11 +480,7 @@ def pa_prefill_paged(out, q, k_pool, v_pool, block_tables, query_start_loc, cont
     return out
 
 
-def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream=None):
-    """Causal attention over whole prompts lying one behind another: q / out are
-    [total, n_q, d], k / v [total, n_kv, d]; sequence s owns rows
-    query_start_loc[s] .. query_start_loc[s + 1] - 1 (int32, on the device).
-    q, k and v may be strided along the tokens (parts of one projection)."""
+def _prefill_packed(fn, out, q, k, v, query_start_loc, scale, dev_err, stream):
     _contig(out, query_start_loc)
     dev = _on_device(q, out, k, v, query_start_loc, dev_err)
     total, n_q, d = q.shape
@@ -482,10 +499,28 @@ def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream
             raise PAError(PA_ERR_INVALID_ARG, "a token's heads must be contiguous")
         # a single token's stride is never used
         strides.append(st[0] if total > 1 else heads * d)
-    _launch(dev, stream, "pa_prefill_packed", lib.pa_prefill_packed, out.data_ptr(), q.data_ptr(),
-            k.data_ptr(), v.data_ptr(), query_start_loc.data_ptr(), scale, n_q, n_kv, d,
+    _launch(dev, stream, "pa_prefill_packed", fn, out.data_ptr(), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), query_start_loc.data_ptr(), scale, n_q, n_kv, d,
             query_start_loc.shape[0] - 1, total, *strides, dtype_code(q), _ptr(dev_err))
     return out
+
+
+def pa_prefill_packed(out, q, k, v, query_start_loc, scale, dev_err=None, stream=None):
+    """Causal attention over whole prompts lying one behind another: q / out are
+    [total, n_q, d], k / v [total, n_kv, d]; sequence s owns rows
+    query_start_loc[s] .. query_start_loc[s + 1] - 1 (int32, on the device).
+    q, k and v may be strided along the tokens (parts of one projection)."""
+    return _prefill_packed(lib.pa_prefill_packed, out, q, k, v, query_start_loc, scale, dev_err,
+                           stream)
+
+
+def pa_test_prefill_packed_timeout(out, q, k, v, query_start_loc, scale, skip_tile: int,
+                                   wait_limit_us: int, dev_err=None, stream=None):
+    """Test hook: pa_prefill_packed with short bounded waits and one K or V tile
+    left unloaded in every CTA, so the waits run out (see include/pa.h)."""
+    def fn(*a):
+        return lib.pa_test_prefill_packed_timeout(*a, int(skip_tile), int(wait_limit_us))
+    return _prefill_packed(fn, out, q, k, v, query_start_loc, scale, dev_err, stream)
 
 
 # --------------------------------------------------------------------------

@@ -31,35 +31,33 @@ constexpr float kRescaleLog2 = 8.f;   // lazy rescale threshold (factor 256)
 // ------------------------------------------------------------------- waits
 // A bounded wait in few instructions (the kernels have dozens of them, and
 // their code would otherwise outgrow the instruction caches): it gives up after
-// a second, or when another role of the CTA has given up.  Giving up flags
-// PA_DEVERR_TIMEOUT.
-constexpr uint32_t kWaitNs = 1000000000u;  // below 2^31: the timer's low word wraps
-
+// p.waits.wait_ns (at most a second, below 2^31: the timer's low word wraps), or
+// when another role of the CTA has given up.  Giving up flags PA_DEVERR_TIMEOUT.
 __device__ __forceinline__ uint32_t timer_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
 
-template <typename Bars>
+template <typename Bars, typename Params>
 __device__ __forceinline__ bool wait_ok(uint64_t* bar, uint32_t parity, Bars* B,
-                                        int32_t* dev_err) {
+                                        const Params& p) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint32_t t0 = timer_lo();
 #pragma unroll 1
   do {
     if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&B->abort_flag)) return false;
-  } while (timer_lo() - t0 < kWaitNs);
-  flag_error(dev_err, PA_DEVERR_TIMEOUT);
+  } while (timer_lo() - t0 < p.waits.wait_ns);
+  flag_error(p.dev_err, PA_DEVERR_TIMEOUT);
   *reinterpret_cast<volatile int*>(&B->abort_flag) = 1;
   return false;
 }
 // the same for a whole warp, which goes on or gives up together
-template <typename Bars>
+template <typename Bars, typename Params>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, Bars* B,
-                                         int32_t* dev_err) {
-  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, dev_err));
+                                         const Params& p) {
+  return __all_sync(0xffffffffu, wait_ok(bar, parity, B, p));
 }
 
 // ------------------------------------------------- two fp32 values at a time

@@ -502,14 +502,15 @@ size_t pa_decode_tree_workspace_size(int num_seqs, int q_len, int n_q_heads, int
   return pa::tree_ws_bytes(q_len, n_q_heads / n_kv_heads, head_dim);
 }
 
-pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
-                         const int32_t* block_tables, const int32_t* context_lens,
-                         const uint64_t* masks, const int32_t* tree_lens, float scale,
-                         int block_size, int n_q_heads, int n_kv_heads, int head_dim,
-                         int num_seqs, int q_len, int max_blocks_per_seq, int num_blocks,
-                         pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale, float v_scale,
-                         void* workspace, size_t workspace_bytes, int32_t* dev_err,
-                         void* stream) {
+static pa_status decode_tree_impl(void* out, const void* q, const void* k_pool,
+                                  const void* v_pool, const int32_t* block_tables,
+                                  const int32_t* context_lens, const uint64_t* masks,
+                                  const int32_t* tree_lens, float scale, int block_size,
+                                  int n_q_heads, int n_kv_heads, int head_dim, int num_seqs,
+                                  int q_len, int max_blocks_per_seq, int num_blocks,
+                                  pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale,
+                                  float v_scale, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_err, void* stream, const pa::WaitParams& waits) {
   const DecodeShape s{n_q_heads, n_kv_heads, head_dim, num_seqs, max_blocks_per_seq, num_blocks, 1};
   const pa_status st = check_decode(s, block_size, q_dtype, kv_dtype);
   if (st != PA_OK) return st;
@@ -550,6 +551,7 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
   p.q_len = q_len;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
+  p.waits = waits;
   p.q_box_nodes = std::min(q_len, 128 / p.group);
   CUtensorMap tmq, tmk, tmv;
   if (!kv_pool_map(k_pool, num_blocks, n_kv_heads, head_dim, kv_dtype, &tmk) ||
@@ -559,6 +561,38 @@ pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const voi
     return PA_ERR_CUDA;
   return cuda_status(pa::launch_tree(p, head_dim, q_dtype == PA_BF16, fp8, workspace, &tmq, &tmk,
                                      &tmv, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_decode_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* context_lens,
+                         const uint64_t* masks, const int32_t* tree_lens, float scale,
+                         int block_size, int n_q_heads, int n_kv_heads, int head_dim,
+                         int num_seqs, int q_len, int max_blocks_per_seq, int num_blocks,
+                         pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale, float v_scale,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                         void* stream) {
+  return decode_tree_impl(out, q, k_pool, v_pool, block_tables, context_lens, masks, tree_lens,
+                          scale, block_size, n_q_heads, n_kv_heads, head_dim, num_seqs, q_len,
+                          max_blocks_per_seq, num_blocks, q_dtype, kv_dtype, k_scale, v_scale,
+                          workspace, workspace_bytes, dev_err, stream, {});
+}
+
+pa_status pa_test_decode_tree_timeout(void* out, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables,
+                                      const int32_t* context_lens, const uint64_t* masks,
+                                      const int32_t* tree_lens, float scale, int block_size,
+                                      int n_q_heads, int n_kv_heads, int head_dim, int num_seqs,
+                                      int q_len, int max_blocks_per_seq, int num_blocks,
+                                      pa_dtype q_dtype, pa_dtype kv_dtype, float k_scale,
+                                      float v_scale, void* workspace, size_t workspace_bytes,
+                                      int32_t* dev_err, void* stream, int skip_tile,
+                                      uint32_t wait_limit_us) {
+  if (skip_tile < 0 || wait_limit_us < 1 || wait_limit_us > 1000000) return PA_ERR_INVALID_ARG;
+  return decode_tree_impl(out, q, k_pool, v_pool, block_tables, context_lens, masks, tree_lens,
+                          scale, block_size, n_q_heads, n_kv_heads, head_dim, num_seqs, q_len,
+                          max_blocks_per_seq, num_blocks, q_dtype, kv_dtype, k_scale, v_scale,
+                          workspace, workspace_bytes, dev_err, stream,
+                          {wait_limit_us * 1000u, skip_tile});
 }
 
 pa_status pa_tree_masks(const int32_t* parents, const int32_t* tree_lens, int num_seqs,
@@ -776,11 +810,12 @@ pa_status pa_prefill_paged(void* out, const void* q, const void* k_pool, const v
                                         static_cast<cudaStream_t>(stream)));
 }
 
-pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
-                            const int32_t* query_start_loc, float scale, int n_q_heads,
-                            int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
-                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
-                            pa_dtype dtype, int32_t* dev_err, void* stream) {
+static pa_status prefill_packed_impl(void* out, const void* q, const void* k, const void* v,
+                                     const int32_t* query_start_loc, float scale, int n_q_heads,
+                                     int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
+                                     int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                     pa_dtype dtype, int32_t* dev_err, void* stream,
+                                     const pa::WaitParams& waits) {
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0) return PA_ERR_INVALID_ARG;
   if (num_seqs < 0 || total_tokens < 0 || !valid_dtype(dtype)) return PA_ERR_INVALID_ARG;
@@ -815,6 +850,7 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
   p.group = n_q_heads / n_kv_heads;
   p.num_seqs = num_seqs;
   p.total = total_tokens;
+  p.waits = waits;
   p.log2_hb = 0;
   while (p.log2_hb < 4 && p.group % (2 << p.log2_hb) == 0) ++p.log2_hb;
   CUtensorMap tmq, tmk, tmv;
@@ -825,6 +861,28 @@ pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void*
     return PA_ERR_CUDA;
   return cuda_status(pa::launch_prompt(p, head_dim, dtype == PA_BF16, &tmq, &tmk, &tmv,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_prefill_packed(void* out, const void* q, const void* k, const void* v,
+                            const int32_t* query_start_loc, float scale, int n_q_heads,
+                            int n_kv_heads, int head_dim, int num_seqs, int total_tokens,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            pa_dtype dtype, int32_t* dev_err, void* stream) {
+  return prefill_packed_impl(out, q, k, v, query_start_loc, scale, n_q_heads, n_kv_heads, head_dim,
+                             num_seqs, total_tokens, q_stride, k_stride, v_stride, dtype, dev_err,
+                             stream, {});
+}
+
+pa_status pa_test_prefill_packed_timeout(void* out, const void* q, const void* k, const void* v,
+                                         const int32_t* query_start_loc, float scale,
+                                         int n_q_heads, int n_kv_heads, int head_dim, int num_seqs,
+                                         int total_tokens, int64_t q_stride, int64_t k_stride,
+                                         int64_t v_stride, pa_dtype dtype, int32_t* dev_err,
+                                         void* stream, int skip_tile, uint32_t wait_limit_us) {
+  if (skip_tile < 0 || wait_limit_us < 1 || wait_limit_us > 1000000) return PA_ERR_INVALID_ARG;
+  return prefill_packed_impl(out, q, k, v, query_start_loc, scale, n_q_heads, n_kv_heads, head_dim,
+                             num_seqs, total_tokens, q_stride, k_stride, v_stride, dtype, dev_err,
+                             stream, {wait_limit_us * 1000u, skip_tile});
 }
 
 pa_status pa_reshape_and_cache(void* k_pool, void* v_pool, const void* key, const void* value,

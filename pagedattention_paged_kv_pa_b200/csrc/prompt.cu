@@ -98,9 +98,9 @@ using attn::wait_ok;
 // The item stream as one role reads it.
 struct Reader {
   int k = 0;
-  __device__ __forceinline__ bool next(Bars* B, int32_t* dev_err, Item& it) {
+  __device__ __forceinline__ bool next(Bars* B, const PromptParams& p, Item& it) {
     const int slot = k % kItems;
-    if (!wait_ok(&B->item_full[slot], (k / kItems) & 1, B, dev_err)) return false;
+    if (!wait_ok(&B->item_full[slot], (k / kItems) & 1, B, p)) return false;
     it = B->items[slot];
     ++k;
     return it.start >= 0;
@@ -235,34 +235,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p, it))) {
       if (lane == 0) rd.done(B);
       __syncwarp();
       const int n = max(it.nkt[0], it.nkt[1]), mine = x ? it.nkt[1] : it.nkt[0];
       const int ends = last_parts(it, x, QT);  // of the last key tile
-      if (mine > 0) ok = wait_all(&B->q_full[x], items & 1, B, p.dev_err);
+      if (mine > 0) ok = wait_all(&B->q_full[x], items & 1, B, p);
       for (int j = 0; j <= n && ok; ++j, c += 2) {
         const uint32_t cv = c - 1;
         const int sk = c % NS, sv = cv % NS;
         const bool do_pv = j > 0 && j <= mine, do_s = j < mine;
         const uint64_t v = dV + sv * kOpStep, k = dK + sk * kOpStep;
         const uint32_t par = (tiles - 1) & 1;
-        if (j > 0) ok = wait_all(&B->full[sv], (cv / NS) & 1, B, p.dev_err);
-        if (j < n) ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p.dev_err);
+        if (j > 0) ok = wait_all(&B->full[sv], (cv / NS) & 1, B, p);
+        if (j < n) ok = ok && wait_all(&B->full[sk], (c / NS) & 1, B, p);
         if (L::kSepP && do_s) {  // S beside P: as soon as the softmax has read the last S
-          if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+          if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p);
           if (!ok) break;
           scores(k, j == mine - 1, j == mine - 1 ? ends : 4);
         }
         if (do_pv) {
           if (j == 1 && items > 0)
-            ok = ok && wait_all(&B->o_free[x], (items - 1) & 1, B, p.dev_err);
-          ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+            ok = ok && wait_all(&B->o_free[x], (items - 1) & 1, B, p);
+          ok = ok && wait_all(&B->p_half[x], par, B, p);
         }
         // (an item's first S goes ahead out of turn)
         if (kTurns && j > 0) {
           if (x > 0 || turns > 0)
-            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p);
           ++turns;
         }
         if (!ok) break;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (j == 1 && kk == 0) ? 0u : 1u);
           }
           __syncwarp();
-          ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+          ok = wait_all(&B->p_full[x], par, B, p);
           if (!ok) break;
           tc::fence_after();
           if (tc::elect_one()) {
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (issued) {
       if (tc::elect_one()) tc::commit(&B->done[x]);
       __syncwarp();
-      mbar_wait(&B->done[x], 0);
+      mbar_wait(&B->done[x], 0, p.waits.wait_ns);
     }
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
@@ -319,8 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nq0 = 0, nq1 = 0;  // Q tiles of A and B
       auto tile = [&](const CUtensorMap* map, int kvh, int row, bool tail) {
         const int st = c % NS;
-        if (c >= (uint32_t)NS && !wait_ok(&B->empty[st], ((c / NS) - 1) & 1, B, p.dev_err))
+        if (c >= (uint32_t)NS && !wait_ok(&B->empty[st], ((c / NS) - 1) & 1, B, p))
           return false;
+        if (c == (uint32_t)p.waits.skip_tile) {
+          ++c;
+          return true;
+        }
         uint8_t* d = smem + L::kKVOff + st * L::kOp;
         // the arrival of a V tile with a tail to zero is warp 12's
         uint64_t* bar = tail ? &B->raw[st] : &B->full[st];
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto query = [&](int x) {
         if (!ok || (x ? it.nkt[1] : it.nkt[0]) == 0) return;
         int& used = x ? nq1 : nq0;
-        if (used > 0) ok = wait_ok(&B->q_empty[x], (used - 1) & 1, B, p.dev_err);
+        if (used > 0) ok = wait_ok(&B->q_empty[x], (used - 1) & 1, B, p);
         if (!ok) return;
         ++used;
         uint8_t* d = smem + L::kQOff + x * L::kOp;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tma_load_3d(d + h * 16384, &tmq, &B->q_full[x], 64 * h, it.h0,
                           it.start + it.i0 + x * QT);
       };
-      while (ok && rd.next(B, p.dev_err, it)) {
+      while (ok && rd.next(B, p, it)) {
         rd.done(B);
         const int n = max(it.nkt[0], it.nkt[1]), kvh = it.h0 / p.group;
         for (int j = 0; j < n && ok; ++j) {
@@ -357,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
-        mbar_wait(&B->full[u % NS], (u / NS) & 1);
-      if (nq0 > 0) mbar_wait(&B->q_full[0], (nq0 - 1) & 1);
-      if (nq1 > 0) mbar_wait(&B->q_full[1], (nq1 - 1) & 1);
+        mbar_wait(&B->full[u % NS], (u / NS) & 1, p.waits.wait_ns);
+      if (nq0 > 0) mbar_wait(&B->q_full[0], (nq0 - 1) & 1, p.waits.wait_ns);
+      if (nq1 > 0) mbar_wait(&B->q_full[1], (nq1 - 1) & 1, p.waits.wait_ns);
     }
   } else if (warp == kSchedWarp) {
     // ------------------------------------------------------------ scheduler
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int slot = k % kItems;
-      bool ok = k < kItems || wait_ok(&B->item_empty[slot], (k / kItems - 1) & 1, B, p.dev_err);
+      bool ok = k < kItems || wait_ok(&B->item_empty[slot], (k / kItems - 1) & 1, B, p);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
         B->items[slot] = it;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Reader rd;
     Item it;
     uint32_t c = 0, phase = 0;  // stages used; per stage, the parity of its next tail
-    while (__all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+    while (__all_sync(0xffffffffu, rd.next(B, p, it))) {
       __syncwarp();
       if (lane == 0) rd.done(B);
       const int n = max(it.nkt[0], it.nkt[1]);
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int valid = it.len - (n - 1) * kTileN;  // rows of the last tile
       if (valid >= kTileN) continue;
       const int st = (c - 1) % NS;
-      if (!wait_all(&B->raw[st], (phase >> st) & 1, B, p.dev_err)) break;
+      if (!wait_all(&B->raw[st], (phase >> st) & 1, B, p)) break;
       phase ^= 1u << st;
       uint8_t* d = smem + L::kKVOff + st * L::kOp;
       // 128-byte rows; the swizzle stays within a row
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     int t = 0, n_mine = 0;
     bool ok = true;
-    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, it))) {
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p, it))) {
       __syncwarp();
       if (lane == 0) rd.done(B);
       const int nkt = x ? it.nkt[1] : it.nkt[0];
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = qw < it.len;
       attn::RowState st{-INFINITY, 0.f};
       for (int j = 0; j < nkt; ++j, ++t) {
-        ok = wait_all(&B->s_full[x], t & 1, B, p.dev_err);
+        ok = wait_all(&B->s_full[x], t & 1, B, p);
         if (!ok) break;
         if (live) {  // rows behind the sequence: nothing reads their P or O
           tc::fence_after();
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // tile came after it
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             if (L::kSepP)
-              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
             if (!ok) break;
             tc::fence_after();
             attn::rescale_o(tO, D, alpha);
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < parts) {  // no row of the tile sees the rest
               st.l += attn::tile_weights<BF16, 32>(s + 32 * c, sle, neg_m, pk);
               if (L::kSepP && c == 0 && t > 0) {  // P of the tile before has been read
-                ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+                ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
                 if (!ok) break;
                 tc::fence_after();
               }
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&B->s_empty[x]);
             // not ahead of the other warps' P of the tile before
             if (t > 0)
-              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
             if (!ok) break;
           }
           mbar_arrive(&B->p_half[x]);
@@ -579,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      ok = wait_all(&B->o_full[x], n_mine & 1, B, p.dev_err);
+      ok = wait_all(&B->o_full[x], n_mine & 1, B, p);
       if (!ok) break;
       ++n_mine;
       const bool valid = qi < it.len;

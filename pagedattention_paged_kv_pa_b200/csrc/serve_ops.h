@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "../../include/pa.h"
+#include "pa_internal.h"
 
 namespace pa {
 
@@ -20,6 +21,14 @@ int device_sms();
 // `done` (one per kernel, zero at first) remembers the devices it was set on.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
+// How long the waits of these kernels last, and (skip_tile >= 0) a tile that the
+// load warps of every CTA leave out, as if it had never arrived (the
+// pa_test_*_timeout hooks).
+struct WaitParams {
+  uint32_t wait_ns = (uint32_t)kWaitLimitNs;
+  int skip_tile = -1;
+};
+
 // Whole-prompt attention: sequence s owns rows query_start_loc[s] ..
 // query_start_loc[s + 1] - 1 of q, k, v and out.
 struct PromptParams {
@@ -29,6 +38,7 @@ struct PromptParams {
   float scale_log2;  // scale x log2(e)
   int n_q, n_kv, group, num_seqs, total;
   int log2_hb;       // heads of a tile: the power of two in the group size, <= 16
+  WaitParams waits;  // skip_tile counts a CTA's K and V tiles
 };
 // tmq: 3-D map over q viewed as [total][n_q][D], box {64, 2^log2_hb, 128 /
 // 2^log2_hb}; tmk / tmv: over k and v viewed as [total][n_kv][D], box {64, 1,
@@ -47,6 +57,7 @@ struct TreeParams {
   float out_mul;     // v_scale for fp8 caches, else 1
   int n_q, n_kv, group, num_seqs, q_len, max_blocks, num_blocks;
   int q_box_nodes;  // nodes of the query map's box
+  WaitParams waits;  // skip_tile counts a CTA's K tiles
   // set by launch_tree
   float* ws_o;     // [CTA][2 slots][rows][D] unnormalised segment outputs
   float2* ws_ml;   // [CTA][2 slots][rows] (log2-domain maximum, sum)

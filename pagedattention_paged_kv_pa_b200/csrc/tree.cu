@@ -129,9 +129,9 @@ using attn::wait_ok;
 // The segment stream as one role reads it.
 struct Reader {
   int k = 0;
-  __device__ __forceinline__ bool next(Bars* B, int32_t* dev_err, Seg& g) {
+  __device__ __forceinline__ bool next(Bars* B, const TreeParams& p, Seg& g) {
     const int slot = k % kSegs;
-    if (!wait_ok(&B->seg_full[slot], (k / kSegs) & 1, B, dev_err)) return false;
+    if (!wait_ok(&B->seg_full[slot], (k / kSegs) & 1, B, p)) return false;
     g = B->segs[slot];
     ++k;
     return g.s >= 0;
@@ -427,13 +427,13 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         }
         __syncwarp();
       };
-      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p, g))) {
         if (lane == 0) rd.done(B);
         __syncwarp();
         const int nt = g.t1 - g.t0, n = SPLIT ? (nt + 1) / 2 : nt;  // A always has a tile
         const int mine = x == 0 ? n : (SPLIT ? nt / 2 : (tile_nodes(g, 1) > 0 ? nt : 0));
         if (SPLIT || mine > 0)
-          ok = wait_all(&B->q_full[qx], (SPLIT ? segs : items) & 1, B, p.dev_err);
+          ok = wait_all(&B->q_full[qx], (SPLIT ? segs : items) & 1, B, p);
         // (split: a tile without a step is done with Q)
         if (SPLIT && mine == 0 && lane == 0) mbar_arrive(&B->q_empty[0]);
         const uint32_t before = SPLIT ? segs : items;  // O_X read out so often
@@ -446,20 +446,20 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           const int sk = ck % KS, sv = cv % VS;
           const uint64_t v = dV + sv * kOpStep, k = dK + sk * kOpStep;
           const uint32_t par = (tiles - 1) & 1;
-          if (use_v) ok = wait_all(&B->v_full[sv], (cv / VS) & 1, B, p.dev_err);
-          if (use_k) ok = ok && wait_all(&B->k_full[sk], (ck / KS) & 1, B, p.dev_err);
+          if (use_v) ok = wait_all(&B->v_full[sv], (cv / VS) & 1, B, p);
+          if (use_k) ok = ok && wait_all(&B->k_full[sk], (ck / KS) & 1, B, p);
           if (L::kSepP && do_s) {  // S beside P: as soon as the softmax has read the last S
-            if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p.dev_err);
+            if (tiles > 0) ok = ok && wait_all(&B->s_empty[x], (tiles - 1) & 1, B, p);
             if (!ok) break;
             scores(k, j == mine - 1);
           }
           if (do_pv) {
-            ok = ok && wait_all(&B->p_half[x], par, B, p.dev_err);
+            ok = ok && wait_all(&B->p_half[x], par, B, p);
             if (j == 1 && before > 0)
-              ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p.dev_err);
+              ok = ok && wait_all(&B->o_free[x], (before - 1) & 1, B, p);
           }
           if (kTurns && (x > 0 || turns > 0))
-            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p.dev_err);
+            ok = ok && wait_all(&B->turn[x], (turns - 1 + x) & 1, B, p);
           if (!ok) break;
           if (do_pv) {
             tc::fence_after();
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
                            (j == 1 && kk == 0) ? 0u : 1u);
             }
             __syncwarp();
-            ok = wait_all(&B->p_full[x], par, B, p.dev_err);
+            ok = wait_all(&B->p_full[x], par, B, p);
             if (!ok) break;
             tc::fence_after();
             if (tc::elect_one()) {
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       if (issued) {
         if (tc::elect_one()) tc::commit(&B->done[x]);
         __syncwarp();
-        mbar_wait(&B->done[x], 0);
+        mbar_wait(&B->done[x], 0, p.waits.wait_ns);
       }
     } else if (warp >= kLoadWarp && warp < kLoadWarp + 4) {
       // ---------------------------------------------------------------- loads
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       bool ok = true;
       uint32_t c = 0;
       int nq[2] = {0, 0};
-      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
         int id = block_id(p, g, g.t0, half, lane);
@@ -534,15 +534,16 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           // the next tile's block ids arrive while this tile waits for a stage
           const int id_next = t + 1 < g.t1 ? block_id(p, g, t + 1, half, lane) : -1;
           const int st = c % NS;
-          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p);
           if (!ok) break;
-          load_tile<D, FP8>(p, g, t, half, ring + st * kStage, map, pool, &full[st], lane, id,
-                            !vop, policy);
+          if (vop || c != (uint32_t)p.waits.skip_tile)
+            load_tile<D, FP8>(p, g, t, half, ring + st * kStage, map, pool, &full[st], lane, id,
+                              !vop, policy);
           id = id_next;
           if (SPLIT && !FP8 && t + 1 == g.t1 && ((g.t1 - g.t0) & 1)) {  // B's empty stage
             ++c;
             const int se = c % NS;
-            if (c >= (uint32_t)NS) ok = wait_all(&empty[se], (c / NS - 1) & 1, B, p.dev_err);
+            if (c >= (uint32_t)NS) ok = wait_all(&empty[se], (c / NS - 1) & 1, B, p);
             if (!ok) break;
             if (lane == 0) mbar_arrive(&full[se]);
           }
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
 #pragma unroll
             for (int x = 0; x < L::kQ; ++x) {
               if (!ok || tile_nodes(g, x) == 0) continue;
-              if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
+              if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p);
               if (!ok) continue;
               ++nq[x];
               if (lane == 0) {
@@ -569,11 +570,11 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       }
       // loads in flight land before the CTA exits
       for (uint32_t u = c > (uint32_t)NS ? c - NS : 0; u < c; ++u)
-        mbar_wait(&full[u % NS], (u / NS) & 1);
+        mbar_wait(&full[u % NS], (u / NS) & 1, p.waits.wait_ns);
       if (q_too)
 #pragma unroll
         for (int x = 0; x < L::kQ; ++x)
-          if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1);
+          if (nq[x] > 0) mbar_wait(&B->q_full[x], (nq[x] - 1) & 1, p.waits.wait_ns);
     } else if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
       int first;
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         }
         if (!emit) continue;
         const int slot = k % kSegs;
-        const bool ok = k < kSegs || wait_ok(&B->seg_empty[slot], (k / kSegs - 1) & 1, B, p.dev_err);
+        const bool ok = k < kSegs || wait_ok(&B->seg_empty[slot], (k / kSegs - 1) & 1, B, p);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lane == 0) {
           B->segs[slot] = g;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       bool ok = true;
       uint32_t c = 0, cr = 0;  // operand tiles, raw tiles
       int nq[2] = {0, 0};
-      while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+      while (ok && __all_sync(0xffffffffu, rd.next(B, p, g))) {
         __syncwarp();
         if (lane == 0) rd.done(B);
         // the K converters write the segment's query rows first
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           if (vop || !ok || nodes == 0) continue;
           // S of the segment before is done: its rows are done with, and the
           // exponents of the one before that have been read (its P was written)
-          if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p.dev_err);
+          if (nq[x] > 0) ok = wait_all(&B->q_empty[x], (nq[x] - 1) & 1, B, p);
           if (!ok) continue;
           const int ri = ct / G, node = (SPLIT ? 0 : 2 * rg + x) * QT + ri;
           write_query_row<BF16, D>(
@@ -671,8 +672,8 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         }
         for (int t = g.t0; t < g.t1 && ok; ++t, ++c, ++cr) {
           const int st = c % NS, rs = cr % RS;
-          bool w = wait_ok(&B->raw_full[vop][rs], (cr / RS) & 1, B, p.dev_err);
-          w = w && (c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p.dev_err));
+          bool w = wait_ok(&B->raw_full[vop][rs], (cr / RS) & 1, B, p);
+          w = w && (c < (uint32_t)NS || wait_ok(&empty[st], (c / NS - 1) & 1, B, p));
           ok = __all_sync(0xffffffffu, w);
           if (!ok) break;
           const uint8_t* src = smem + L::kRawOff + ((vop ? RS : 0) + rs) * L::kRaw;
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         }
         if (SPLIT && ok && ((g.t1 - g.t0) & 1)) {  // B's empty stage
           const int st = c % NS;
-          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p.dev_err);
+          if (c >= (uint32_t)NS) ok = wait_all(&empty[st], (c / NS - 1) & 1, B, p);
           if (ok) mbar_arrive(&full[st]);
           ++c;
         }
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
     Seg g;
     int t = 0, n_mine = 0, n_segs = 0;
     bool ok = true;
-    while (ok && __all_sync(0xffffffffu, rd.next(B, p.dev_err, g))) {
+    while (ok && __all_sync(0xffffffffu, rd.next(B, p, g))) {
       __syncwarp();
       if (lane == 0) rd.done(B);
       const int nodes = tile_nodes(g, x);
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       const int nt = g.t1 - g.t0;
       bool any = false;
       for (int ti = SPLIT ? x : 0; ti < nt; ti += SPLIT ? 2 : 1, ++t) {
-        ok = wait_all(&B->s_full[x], t & 1, B, p.dev_err);
+        ok = wait_all(&B->s_full[x], t & 1, B, p);
         if (!ok) break;
         if (FP8 && !any)  // the row went in times 2^e
           sl *= exp2i(-reinterpret_cast<int8_t*>(
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
           // tile came after it
           if (any && __any_sync(0xffffffffu, grow)) {
             if (L::kSepP)
-              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
             if (!ok) break;
             tc::fence_after();
             attn::rescale_o(tO, D, alpha);
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
             }
             l += attn::tile_weights<kOpBf16, 64>(s + (L::kLean ? 0 : 64 * h), sle, neg_m, pk);
             if (L::kSepP && h == 0 && t > 0) {  // P of the tile before has been read
-              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
               if (!ok) break;
               tc::fence_after();
             }
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
             mbar_arrive(&B->s_empty[x]);
             // not ahead of the other warps' P of the tile before
             if (t > 0)
-              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p.dev_err);
+              ok = wait_all(&B->pv_done[x], (t - 1) & 1, B, p);
             if (!ok) break;
           }
           mbar_arrive(&B->p_half[x]);
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
       if (!ok) break;
       // ------------------------------------------------ segment epilogue
       if (any) {
-        ok = wait_all(&B->o_full[x], n_mine & 1, B, p.dev_err);
+        ok = wait_all(&B->o_full[x], n_mine & 1, B, p);
         if (!ok) break;
         ++n_mine;
       }
@@ -845,12 +846,12 @@ __global__ void __launch_bounds__(FP8 ? 768 : 512, 1)
         float2* red = reinterpret_cast<float2*>(smem + L::kRedOff) + r;
         // (the segment before was read out by both)
         if (seg > 0)
-          ok = wait_all(&B->o_free[0], (seg - 1) & 1, B, p.dev_err);
+          ok = wait_all(&B->o_free[0], (seg - 1) & 1, B, p);
         if (!ok) break;
         red[x * 128] = make_float2(m, l);
         tc::fence_before();
         mbar_arrive(&B->red[x]);
-        ok = wait_all(&B->red[x ^ 1], seg & 1, B, p.dev_err);
+        ok = wait_all(&B->red[x ^ 1], seg & 1, B, p);
         if (!ok) break;
         const float2 a = red[0], b = red[128];
         m = fmaxf(a.x, b.x);

@@ -255,3 +255,13 @@ def test_overlapping_memory_is_refused(B):
     assert _compact(B, k=apart[:2], v=[apart[2], apart[2] + pool - 16]) == B.PA_ERR_INVALID_ARG
     many = [pool * i + 16 for i in range(1, 201)]
     assert _compact(B, k=many[:100], v=many[100:199] + many[:1]) == B.PA_ERR_INVALID_ARG
+
+
+def test_timeout_hook_refusals(B):
+    for skip, limit in ((-1, 2000), (0, 0), (0, 1_000_001)):
+        assert B.lib.pa_test_prefill_packed_timeout(
+            *[V(16)] * 5, 0.1, 8, 2, 128, 3, 50, 1024, 256, 256, B.PA_BF16, None, None, skip,
+            limit) == B.PA_ERR_INVALID_ARG
+        assert B.lib.pa_test_decode_tree_timeout(
+            *[V(16)] * 7, None, 0.1, 16, 8, 2, 128, 4, 10, 40, 100, B.PA_BF16, B.PA_BF16, 1.0, 1.0,
+            V(16), 1 << 40, None, None, skip, limit) == B.PA_ERR_INVALID_ARG

@@ -59,3 +59,63 @@ def test_the_hook_refuses_bad_arguments(B, cuda_device):
             B.pa_test_decode_timeout(out, d.q, d.k_pool, d.v_pool, d.block_tables,
                                      d.context_lens, d.scale, skip_tile=skip,
                                      wait_limit_us=limit)
+
+
+# The same of whole-prompt and tree attention, whose CTAs have a dozen warps or
+# more that wait on one another: whichever waits for the missing tile gives up
+# first and the others follow it.
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("skip", [0, 1, 4, 7])
+def test_prompt_waits_that_run_out(B, cuda_device, d, skip):
+    # prompts of 1 to 6 key tiles, each with a last V tile whose end is zeroed
+    from tests import test_prefill_packed_gpu as T
+    lens = [700, 90, 300, 1, 650, 128]
+    q, k, v, start = T.make(lens, 16, 2, d, torch.bfloat16, cuda_device, seed=502)
+    want, err = T.run(B, q, k, v, start, 0.09)
+    assert err == 0
+    out = torch.empty_like(want)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    t0 = time.monotonic()
+    B.pa_test_prefill_packed_timeout(out, q, k, v, start, 0.09, skip_tile=skip,
+                                     wait_limit_us=2000, dev_err=err)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < 30
+    assert int(err.item()) == PA_DEVERR_TIMEOUT
+    got, err = T.run(B, q, k, v, start, 0.09)
+    assert err == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [6, 40])  # one tile of rows, and two
+@pytest.mark.parametrize("skip", [0, 3])
+def test_tree_waits_that_run_out(B, cuda_device, fp8, d, nodes, skip):
+    from tests import test_decode_tree_gpu as T
+    c = T.Case([9000, 200, 6100, 77] * 4, nodes, 16, 4, d, torch.bfloat16, fp8, cuda_device,
+               seed=503)
+    want = c.run(B)
+    a, k = c.args()
+    out = torch.empty_like(want)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    t0 = time.monotonic()
+    B.pa_test_decode_tree_timeout(out, *a, skip_tile=skip, wait_limit_us=2000, dev_err=err, **k)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < 30
+    assert int(err.item()) == PA_DEVERR_TIMEOUT
+    assert torch.equal(c.run(B), want)
+
+
+def test_the_attention_hooks_refuse_bad_arguments(B, cuda_device):
+    from tests import test_decode_tree_gpu as T
+    from tests import test_prefill_packed_gpu as TP
+    q, k, v, start = TP.make([40], 4, 2, 64, torch.bfloat16, cuda_device)
+    c = T.Case([40], 3, 4, 2, 64, torch.bfloat16, False, cuda_device)
+    a, kw = c.args()
+    for skip, limit in ((-1, 2000), (0, 0), (0, 2_000_000)):
+        with pytest.raises(B.PAError):
+            B.pa_test_prefill_packed_timeout(torch.empty_like(q.contiguous()), q, k, v, start, 0.1,
+                                             skip_tile=skip, wait_limit_us=limit)
+        with pytest.raises(B.PAError):
+            B.pa_test_decode_tree_timeout(torch.empty_like(c.q), *a, skip_tile=skip,
+                                          wait_limit_us=limit, **kw)
