@@ -377,15 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     int start0 = 0, len0 = span_of(p, lane, start0), before0 = 0;
     int top = 0;
     bool ordered = true;
-#pragma unroll 1
-    for (int s = lane, a = start0, n = len0; s < p.num_seqs;) {
+    auto look = [&](int a, int n) {
       // (a negative end gives n < 0 or, wrapped, a + n >= 2^31)
       if (a < 0 || n < 0 || n > p.total - a)
         ordered = false;
       else
         top = max(top, items_of(n));
-      s += 32;
-      n = span_of(p, s, a);
+    };
+    look(start0, len0);
+#pragma unroll 1
+    for (int s = 32 + lane; s < p.num_seqs; s += 32) {
+      int a;
+      const int n = span_of(p, s, a);
+      look(a, n);
     }
     ordered = __all_sync(0xffffffffu, ordered);
     if (!ordered) {
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s0 = 0; s0 < p.num_seqs; s0 += 32)
         top = max(top, items_of(span_in_order(p, s0 + lane, lane, before, start)));
     }
-    for (int m = 16; m >= 1; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+    top = __reduce_max_sync(0xffffffffu, top);
     if (!ordered) len0 = span_in_order(p, lane, lane, before0, start0);
     int level = top, cnt = 0;
     unsigned base = 0;  // (sequence, level) pairs before this level
