@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       Reader rd;
-      Item it;
+      Item it{};
       bool ok = true;
       uint32_t c = 0;
       int nq0 = 0, nq1 = 0;  // Q tiles of A and B
