@@ -673,7 +673,10 @@ pa_status pa_alloc_prepare_write(pa_alloc* a, int64_t seq, int64_t* cow_pairs_ou
  * (with n_tokens 0 it holds no block).  `tokens` gives the ids of its last
  * n_ids tokens, n_tokens - n_ids .. n_tokens - 1 (the accepted ones; n_ids 0:
  * none, tokens may be NULL): when with them every token's id is known, the
- * sequence registers full blocks again (prefix caching).  PA_ERR_INVALID_ARG
+ * sequence registers full blocks again (prefix caching).  So drafted tokens are
+ * appended without ids (pa_alloc_append): given to pa_alloc_append_tokens they
+ * would count as known, and a full block of a tree's nodes would be registered as
+ * if they followed one another.  PA_ERR_INVALID_ARG
  * for an unknown seq, n_tokens or n_ids out of range, or an id that differs
  * from a known one. */
 pa_status pa_alloc_truncate(pa_alloc* a, int64_t seq, int n_tokens, const int32_t* tokens,

@@ -21,7 +21,9 @@
 // whose count reaches zero become cached, released from the sequence's last
 // block to its first (of blocks released together the prefix's tail goes
 // first).  A second block with an already registered prefix stays
-// unregistered; a partial last block is never registered.
+// unregistered; a partial last block is not registered, except one that
+// pa_alloc_truncate cut: it keeps its content, and with it its registration, until
+// the sequence is appended to.
 //
 // Free blocks are handed out first-in first-out, so the state after a call
 // sequence is a deterministic function of the calls.  Each call either does

@@ -166,9 +166,13 @@ __device__ __forceinline__ void rescale_o(uint32_t to, int cols, float alpha) {
   tc::wait_st();
 }
 
-// Weights 2^(x sl - m) of keys K0 .. K0 + NK - 1 into pk as 16-bit pairs; returns
-// their fp32 sum.  Masked scores are -inf, with sl = 1 (tile_max has scaled the
-// others), so that tiles with and without a mask run the same code.
+// Weights 2^(x sl - m) of NK keys into pk as 16-bit pairs; returns their fp32 sum.
+// Masked scores are -inf, with sl = 1 (tile_max has scaled the others), so that
+// tiles with and without a mask run the same code.
+// The pairs are the A operand of O += P V, which has V's 16-bit type (f16 where V is
+// E4M3): each weight is off by at most half a step of it, 2^-8 or 2^-11 of the
+// weight, as much as the output's own rounding.  The sum is of the weights before
+// that, whose errors do not average out in a sum of a few keys.
 template <bool BF16, int NK>
 __device__ __forceinline__ float tile_weights(const float* x, float sl, float neg_m,
                                               uint32_t* pk) {

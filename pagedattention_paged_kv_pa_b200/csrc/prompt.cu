@@ -30,12 +30,16 @@
 //
 // Measured back to back in a CUDA graph (and sustained over seconds, where 128-
 // wide heads run into the power limit): 16,384 tokens of 32/8 heads of 128, bf16,
-// 1.74 ms = 1,261 TFLOP/s of causal products (2.03 ms); 16 prompts of up to 2,100
-// tokens, 64/8 x 128, 313 us = 943 TFLOP/s (371 us); 8 of up to 1,500, 32/8 x 64,
-// 52 us; one of 37 tokens 8.2 us.  What bounds it is each tile's chain P -> O +=
-// P V -> next S -> softmax, ~1,700 clocks for two tiles against 1,024 of the
-// products or the exponentials (tensor pipe and XU at 47 %): at head_dim 128 P
-// lies over S, for want of TMEM.
+// 1.73 ms = 1,273 TFLOP/s of causal products (2.04 ms); 16 prompts of up to 2,100
+// tokens, 64/8 x 128, 311 us = 947 TFLOP/s (370 us); 8 of up to 1,500, 32/8 x 64,
+// 51.4 us; one of 37 tokens 8.0 us, of 1 token 6.5 us.  A tile takes 1,820 clocks
+// on the first (time x SM clock over a CTA's 1,785 tiles) and 2,030 active ones on
+// the second, whose CTAs come to the end of an item 24 times, against 1,024 of
+// either its products or its exponentials (tensor pipe and XU at 47 %).  128-wide
+// heads: the chain P -> O += P V -> next S -> softmax, since P lies over S for want
+// of TMEM.  64-wide heads (P beside S) and short prompts: the ends of items, where
+// the softmax warps write O before they begin the next one (2,600 clocks a tile on
+// the third, 4.7 items a CTA).
 #include <type_traits>
 
 #include "attn_tile.cuh"
@@ -369,7 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ scheduler
     // level = position of an item in its sequence, in items; the levels are
     // walked downwards, within a level the sequences that reach it in order,
-    // and the head groups of each
+    // and the head groups of each.  Only the first 32 sequences are kept, the others
+    // are looked through again for every item: 32/8 heads of 128, prompts of 16 to
+    // 64 tokens, 0.23 us a prompt for 256 of them, 0.30 for 1,024, 1.0 for 4,096
     const unsigned hgroups = p.n_q >> lhb;
     const int lspan = 8 - lhb, span = 1 << lspan;  // queries of an item
     auto items_of = [&](int len) { return (len + span - 1) >> lspan; };

@@ -39,11 +39,11 @@
 // the CTA drains its loads and MMAs and frees TMEM.
 //
 // Measured back to back in a CUDA graph: 64 contexts of up to 8,000 with 16 nodes,
-// 64/8 heads of 128, bf16, 146 us = 5.5 TB/s of K/V (HBM bounds it; over seconds
+// 64/8 heads of 128, bf16, 145 us = 5.5 TB/s of K/V (HBM bounds it; over seconds
 // the power limit, 1,485 MHz and 170 us); 16 of up to 8,191 with 64 nodes 130 us =
 // 735 TFLOP/s (the chain P -> O += P V -> S -> softmax); 96 of up to 4,000 with 24 nodes, 32/8 x 128, E4M3, 135 us = 2.4 TB/s
 // (the chain through the converters; issue 50 %, ALU 41 %); one context of 777 with
-// 8 nodes 14.9 us with the merge (start-up).
+// 8 nodes 14.9 us with the merge, of 8 alone 11.7 us (start-up of two kernels).
 #include <type_traits>
 
 #include "attn_tile.cuh"
@@ -1063,6 +1063,11 @@ cudaError_t launch_tree(TreeParams& p, int D, bool bf16, bool fp8, void* workspa
                         const CUtensorMap* tmq, const CUtensorMap* tmk, const CUtensorMap* tmv,
                         cudaStream_t st) {
   if (p.num_seqs == 0) return cudaSuccess;
+  // The most nodes of the batch choose the kernel: one tile, or two for all (and a
+  // second CTA beside, since TMEM holds two), so that small trees beside a large one
+  // leave B idle.  64 contexts of up to 8,000, 64/8 heads of 128, bf16, trees of 4 to
+  // 16 nodes: 145 us with q_len 16, 174 with 17, 323 with 40; three of them with 40
+  // nodes 368.
   const int qt = kTileM / p.group, tiles = (p.q_len + qt - 1) / qt;
   p.row_groups = tiles > 2 ? 2 : 1;
   p.step_keys = tiles == 1 ? 2 * kTileN : kTileN;
